@@ -14,8 +14,11 @@
  *   pkv_decode_graph_*      a decode step (all layers) captured once per batch-size
  *                           bucket and replayed with one CUDA graph launch
  *   pkv_decode_attn_noalloc decode attention with its split scratch inside the library
+ *   pkv_batch_tables        block tables, slot map, positions and query offsets of a step,
+ *                           built on the GPU from the requests' lengths and a page pool
+ *   pkv_rope                rotary positions of query and key rows (a whole step's tokens)
  *   *_ex                    the decode calls with per-call options (pkv_decode_opts)
- *   *_workspace_size, pkv_status_string                               host helpers
+ *   *_workspace_size, pkv_rope_plan_init, pkv_status_string           host helpers
  *
  * Sources (page title, section):
  *   "Tiny-LLM-Inference Project_Status", feature list and dtype contract: paged KV
@@ -65,6 +68,7 @@
  *                K element (t, d) at ((t/8) * (head_dim/8) + d/8) * 64 + (t%8) * 8 + d%8
  *                V element (t, d) at ((d/8) * 2 + t/8) * 64 + (d%8) * 8 + t%8
  *   k_scale, v_scale  float32 [num_pages][num_kv_heads][page_size]   INT8, FP8, INT4
+ *                     float32 [num_pages][num_kv_heads]              INT8B, FP8B
  *   Token t of a sequence lives in page block_tables[b][t / page_size] at offset
  *   t % page_size; its slot number is page * page_size + offset.
  *   Element types: PKV_F32 float32, PKV_BF16 bfloat16, and three coded formats whose
@@ -76,7 +80,16 @@
  *     PKV_INT4  4-bit two's-complement codes in [-7, 7], scale = max|x| / 7
  *   ("tinyloop Current Status", KV cache modes table: INT8 and INT4 KV caches; the
  *   TinyInfer review, item 2: INT8 or FP8 KV cache).
- *   All cache pointers must be 16-byte aligned.
+ *   Two more 8-bit formats have one scale for each block of 16 tokens (a page) and kv head,
+ *   in the layouts of INT8 and FP8; a block's first append decides its scale, and later
+ *   ones raise it (pkv_append):
+ *     PKV_INT8B codes as PKV_INT8, scale = max|x| / 127 over the block;
+ *     PKV_FP8B  codes as PKV_FP8, scale the smallest power of two (from 2^-126 on) with
+ *               max|x| / scale <= 448
+ *   They serve append, decode (also without scratch, and in decode graphs) and, unlike the
+ *   other coded formats, chunked prefill; pkv_decode_step returns PKV_ERR_UNSUPPORTED,
+ *   because a new row can change its whole block's codes.
+ *   All cache pointers must be 16-byte aligned (the scales of INT8B and FP8B included).
  *
  * Sliding window (pkv_cache.window; "tinyloop Current Status", KV cache modes table: a
  * cache window bounds the KV storage).  With window W > 0 every attention call lets the
@@ -97,7 +110,15 @@
 extern "C" {
 #endif
 
-typedef enum { PKV_F32 = 0, PKV_BF16 = 1, PKV_INT8 = 2, PKV_FP8 = 3, PKV_INT4 = 4 } pkv_dtype;
+typedef enum {
+  PKV_F32 = 0,
+  PKV_BF16 = 1,
+  PKV_INT8 = 2,
+  PKV_FP8 = 3,
+  PKV_INT4 = 4,
+  PKV_INT8B = 5, /* 8 bits, one scale for each block of 16 tokens and kv head */
+  PKV_FP8B = 6
+} pkv_dtype;
 
 typedef enum {
   PKV_OK = 0,
@@ -118,12 +139,13 @@ typedef enum {
 #define PKV_DEV_BAD_SLOT 0x4 /* append slot >= num_pages * page_size */
 #define PKV_DEV_BAD_CHUNK 0x8 /* prefill chunk length < 0 or > context length */
 #define PKV_DEV_TIMEOUT 0x10 /* a bounded wait on an asynchronous copy gave up */
+#define PKV_DEV_NO_PAGES 0x20 /* the page pool ran short of a request's new pages */
 
 typedef struct pkv_cache {
   void* k_cache;
   void* v_cache;
-  float* k_scale; /* INT8, FP8, INT4 only, else NULL */
-  float* v_scale; /* INT8, FP8, INT4 only, else NULL */
+  float* k_scale; /* the coded formats only, else NULL */
+  float* v_scale; /* the coded formats only, else NULL */
   int32_t num_pages;
   int32_t page_size;
   int32_t num_kv_heads;
@@ -144,6 +166,14 @@ typedef struct pkv_cache {
  *                  saturating at +-448.  An all-zero row stores s = 0 and zero codes.
  *   slot_mapping   int32 [num_tokens]; slot < 0 skips that token (padding);
  *                  slot >= num_pages * page_size sets PKV_DEV_BAD_SLOT and is skipped.
+ *                  INT8B / FP8B cache: the call's rows of one page stand next to each
+ *                  other, in ascending order of consecutive slots.  They raise the block's
+ *                  scale as far as their largest value needs it (a run that starts at offset
+ *                  0 starts the scale afresh); when it grows, the rows before the run are
+ *                  coded again at the new scale, code' = round(code * (old / new)) with
+ *                  both operations in float, as their format rounds; rows behind the run
+ *                  keep their bytes.  Rows out of that order set PKV_DEV_BAD_SLOT and are
+ *                  skipped; two separate runs of one page are not allowed.
  *   Slots within one call must be distinct.  num_tokens == 0 is a no-op.
  */
 pkv_status pkv_append(const pkv_cache* cache, const void* k_new, const void* v_new,
@@ -292,8 +322,8 @@ pkv_status pkv_prefill_workspace_size_ex(const pkv_cache* cache, int32_t num_seq
  *   out            float32 [total_q][num_q_heads][head_dim].
  *   workspace      as for decode (pkv_prefill_workspace_size bytes, which covers both
  *                  query types; 0 when no row tile's keys are split).
- * The cache must be PKV_BF16 (other formats return PKV_ERR_UNSUPPORTED); the query tile
- * products run on the tcgen05 tensor cores.
+ * The cache must be PKV_BF16, PKV_INT8B or PKV_FP8B (other formats return
+ * PKV_ERR_UNSUPPORTED); the query tile products run on the tcgen05 tensor cores.
  */
 pkv_status pkv_prefill_chunk_attn(const pkv_cache* cache, const void* q, int32_t q_dtype,
                                   int32_t num_seqs, int32_t num_q_heads,
@@ -432,6 +462,125 @@ int32_t pkv_decode_graph_bucket(const pkv_decode_graph* graph, int32_t num_seqs)
 
 /* Releases the executor's graphs (after its launches have completed); NULL is a no-op. */
 void pkv_decode_graph_destroy(pkv_decode_graph* graph);
+
+/*
+ * The tables of one serving step, built on the GPU from the requests' lengths.  (The pages
+ * name 16-token pages and chunked prefill/decode scheduling, "Tiny-LLM-Inference
+ * Project_Status", feature list, and no mechanism.)  Every other call reads block tables,
+ * slots, context lengths, positions and query offsets; this one makes them all, in one
+ * launch and without a copy to the host, so a step can be replayed from a CUDA graph.
+ *
+ * The pool.  ring holds page ids; the free ones are the state[1] entries from state[0] on,
+ * wrapping at num_pages.  Pages are taken from its front and returned behind its end.  A new
+ * pool of N pages is ring = {0 .. N-1} and state = {0, N, 0, 0}.  state[2] is zero between
+ * calls (a ticket the call's blocks use); state[3] is not used.  Calls on one pool must be
+ * ordered (one stream, or events).
+ *
+ *   cached_lens    int32 [num_seqs]: tokens of request b already in cache; its block table
+ *                  names the pages of those
+ *   new_lens       int32 [num_seqs]: its new tokens of this step, 0 for none, < 0: it has
+ *                  ended and its pages are returned (its table row is left as it is; the
+ *                  caller sets cached_lens to 0 before the row is used again, and returns
+ *                  no page that another table still names).  Entries that are negative
+ *                  (pages released before a window) are passed over.
+ *   block_tables   int32 [num_seqs][max_blocks_per_seq], in and out: entries of new pages
+ *                  are written, the others left as they are
+ *   context_lens   int32 [num_seqs], out: cached + new tokens, as the attention calls take
+ *                  them; 0 for requests that ended or were not served.  Must not be
+ *                  cached_lens or new_lens themselves (PKV_ERR_UNSUPPORTED).
+ *   q_start_loc    int32 [num_seqs + 1], out, or NULL: first row of every request
+ *   positions      int32 [max_tokens], out, or NULL: each row's position
+ *   slot_mapping   int32 [max_tokens], out: each row's slot, page * 16 + offset
+ *   max_tokens     rows of the two: those behind the last request's, and the rows of
+ *                  requests that were not served, get position -1 and slot -1
+ * Requests are served in order.  One that needs no new page is always served; one that
+ * needs some is served while the pages needed up to and with it fit the free ones
+ * (else PKV_DEV_NO_PAGES).  Lengths below zero or beyond the table, and rows beyond
+ * max_tokens, are not served (PKV_DEV_BAD_LEN); a row whose page id is outside the pool
+ * gets slot -1 (PKV_DEV_BAD_PAGE), as does an impossible pool state or a page returned to a
+ * full pool.  The pool is untouched by requests that are not served.
+ */
+typedef struct pkv_page_pool {
+  int32_t* ring;      /* [num_pages] */
+  int32_t* state;     /* [4] */
+  int32_t num_pages;
+  int32_t page_size;
+} pkv_page_pool;
+
+pkv_status pkv_batch_tables(const pkv_page_pool* pool, const int32_t* cached_lens,
+                            const int32_t* new_lens, int32_t num_seqs, int32_t* block_tables,
+                            int32_t max_blocks_per_seq, int32_t* context_lens,
+                            int32_t* q_start_loc, int32_t* positions, int32_t* slot_mapping,
+                            int32_t max_tokens, int32_t* dev_status, void* stream);
+
+/*
+ * Rotary positions ("tinyloop Current Status", model architecture support table: RoPE in
+ * every forward path with a configurable theta; no formula given).  pkv_decode_step rotates
+ * a decode step's rows itself; this call serves prefill chunks, other layouts, partly
+ * rotated heads, contexts beyond the trained length, and gradients.
+ *   Pair i of a head, i < rotary_dim / 2, is (x_i, x_{i + rotary_dim/2}) (PKV_ROPE_HALF)
+ *   or (x_{2i}, x_{2i+1}) (PKV_ROPE_INTERLEAVED) and becomes
+ *     m (a cos t - b sin t),  m (b cos t + a sin t),   t = position * f_i,
+ *   m the attention_factor; columns from rotary_dim on are copied.  transposed turns by
+ *   -t: the gradient with respect to the rows is the transposed turn of the output's.
+ *   f_i by scaling (f = theta^(-2i / rotary_dim)):
+ *     PKV_ROPE_NONE     f
+ *     PKV_ROPE_LINEAR   f / factor
+ *     PKV_ROPE_BASE     f of theta * factor^(rotary_dim / (rotary_dim - 2))
+ *     PKV_ROPE_BANDS    g f + (1 - g) f / factor, g = (r - low) / (high - low) limited to
+ *                       [0, 1], r = original_len * f / 2 pi the pair's turns over the
+ *                       trained length: fast pairs keep f, slow ones are stretched
+ *   Frequencies are kept to 2^-64 of a turn (and 53 bits), and angles are exact for them,
+ *   whatever the position; the turn is computed in float and rounded once to the rows' type.
+ */
+typedef enum { PKV_ROPE_HALF = 0, PKV_ROPE_INTERLEAVED = 1 } pkv_rope_layout;
+typedef enum {
+  PKV_ROPE_NONE = 0,
+  PKV_ROPE_LINEAR = 1,
+  PKV_ROPE_BASE = 2,
+  PKV_ROPE_BANDS = 3
+} pkv_rope_scaling;
+#define PKV_ROPE_MAX_PAIRS 128
+
+typedef struct pkv_rope_params {
+  int32_t rotary_dim;      /* even, 2 .. head_dim */
+  int32_t layout;          /* pkv_rope_layout */
+  int32_t transposed;      /* nonzero: turn by the opposite angle */
+  int32_t scaling;         /* pkv_rope_scaling */
+  double theta;            /* > 1 */
+  double factor;           /* >= 1 (LINEAR, BASE, BANDS) */
+  double low, high;        /* 0 <= low < high, in turns (BANDS) */
+  int32_t original_len;    /* >= 1 (BANDS) */
+  float attention_factor;  /* >= 0; 0 means 1 */
+} pkv_rope_params;
+
+/* Host memory, filled by pkv_rope_plan_init and kept by the caller. */
+typedef struct pkv_rope_plan {
+  int32_t rotary_dim, layout, transposed;
+  float attention_factor;
+  uint64_t freq[PKV_ROPE_MAX_PAIRS]; /* turns per position, as a fraction of 2^64 */
+} pkv_rope_plan;
+
+/* Host call: the frequencies of a description (PKV_ERR_SHAPE if it is out of range). */
+pkv_status pkv_rope_plan_init(const pkv_rope_params* params, pkv_rope_plan* plan);
+
+/*
+ * Turns num_tokens rows of queries and keys.
+ *   q, k           [num_tokens][heads][head_dim], element type dtype (PKV_F32 or PKV_BF16);
+ *                  q_stride, k_stride are the elements from one token to the next (0: rows
+ *                  without gaps), so that views of a fused projection are taken as they are.
+ *                  Either may have no heads (NULL).  head_dim at most 256.
+ *   q_out, k_out   the same shapes with strides of their own; equal to the inputs (with the
+ *                  same strides) to turn in place, and otherwise not overlapping them
+ *   positions      int32 [num_tokens]; a row at a negative position is padding and is not
+ *                  read or written
+ * Any alignment of the rows' element type is taken; 16-byte vectors are used when bases,
+ * strides, head_dim and rotary_dim / 2 allow.
+ */
+pkv_status pkv_rope(const pkv_rope_plan* plan, const void* q, void* q_out, int64_t q_stride,
+                    int64_t q_out_stride, int32_t num_q_heads, const void* k, void* k_out,
+                    int64_t k_stride, int64_t k_out_stride, int32_t num_kv_heads, int32_t dtype,
+                    int32_t num_tokens, int32_t head_dim, const int32_t* positions, void* stream);
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char* pkv_status_string(pkv_status status);

@@ -14,7 +14,7 @@ namespace pkv {
 
 pkv_status check_cache(const pkv_cache* c) {
   if (!c || !c->k_cache || !c->v_cache) return PKV_ERR_NULL;
-  if (c->kv_dtype < PKV_F32 || c->kv_dtype > PKV_INT4) return PKV_ERR_DTYPE;
+  if (c->kv_dtype < PKV_F32 || c->kv_dtype > PKV_FP8B) return PKV_ERR_DTYPE;
   if (c->page_size != 16) return PKV_ERR_PAGE_SIZE;
   if (c->num_pages < 1 || c->num_kv_heads < 1 || c->head_dim < 1) return PKV_ERR_SHAPE;
   if (c->window < 0) return PKV_ERR_SHAPE;
@@ -136,10 +136,13 @@ pkv_status pkv_decode_workspace_size_ex(const pkv_cache* cache, int32_t num_seqs
   if (!pkv::split_pages_of(opts, &split)) return PKV_ERR_SHAPE;
   int dev = 0;
   if ((s = current_device(&dev)) != PKV_OK) return s;
-  // one size for both pkv_decode_attn and pkv_decode_step (their plans may differ)
+  // one size for both pkv_decode_attn and pkv_decode_step (their plans may differ; the
+  // block-scaled formats have no fused step)
   pkv::DecodePlan plan{}, plan_step{};
   if (!pkv::plan_decode(view(cache), num_seqs, num_q_heads, max_blocks_per_seq, PKV_F32, dev,
-                        split, &plan) ||
+                        split, &plan))
+    return PKV_ERR_DEVICE;
+  if (!pkv::block_scaled(cache->kv_dtype) &&
       !pkv::plan_decode(view(cache), num_seqs, num_q_heads, max_blocks_per_seq, PKV_F32, dev,
                         split, &plan_step, true))
     return PKV_ERR_DEVICE;
@@ -208,6 +211,7 @@ pkv_status pkv_decode_step_ex(const pkv_cache* cache, const void* q, int32_t q_d
   if (s != PKV_OK) return s;
   if (q_dtype != PKV_F32 && q_dtype != PKV_BF16) return PKV_ERR_DTYPE;
   if (new_dtype != PKV_F32 && new_dtype != PKV_BF16) return PKV_ERR_DTYPE;
+  if (pkv::block_scaled(cache->kv_dtype)) return PKV_ERR_UNSUPPORTED;
   if (positions && !(rope_theta > 1.0)) return PKV_ERR_SHAPE;
   int split = 0;
   if (!pkv::split_pages_of(opts, &split)) return PKV_ERR_SHAPE;

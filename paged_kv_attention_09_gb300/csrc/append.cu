@@ -115,6 +115,178 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
 }
 
+// Block-scaled 8-bit formats: the scale belongs to the 16 tokens of a (page, kv head), so
+// the new rows of one page are taken together.  They stand next to each other in the call in
+// ascending order of their slots (a run); the run's first token leads: one warp per (leader,
+// kv head, K or V) finds the largest new value, grows the block's scale to hold it (rows
+// before the run's first offset keep their place and are coded again when it grows; a run
+// that starts the page starts its scale afresh), and stores the run.  The other tokens'
+// warps leave at once.
+//
+// The old block is fetched whole, 16 bytes a lane, together with the new rows, before the
+// scale is known: a decode step's append then waits for one round trip after the slots'.
+// A V block has its tokens along the rows, so its bytes are merged in registers and stored
+// as whole 16-byte rows; K rows are stored as they are, old rows only when coded again.
+template <bool FP8, int NEW_DT, int D>
+__global__ void __launch_bounds__(kWarps * 32)
+    append_block_kernel(uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache,
+                        float* __restrict__ k_scale, float* __restrict__ v_scale,
+                        const void* __restrict__ k_new, const void* __restrict__ v_new,
+                        const int32_t* __restrict__ slots, int T, int Hkv, int num_pages,
+                        int32_t* dev_status) {
+  constexpr int E = D / 32;  // head-dim elements per lane; also 16-byte pieces of a block
+  const int lane = threadIdx.x & 31;
+  const long long item = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int which = static_cast<int>(item & 1);
+  const long long th = item >> 1;
+  if (th >= static_cast<long long>(T) * Hkv) return;
+  const int tok = static_cast<int>(th / Hkv), h = static_cast<int>(th % Hkv);
+  // slots of this token, the one before (lane 16) and the 15 after it (lanes 1 .. 15)
+  const int idx = lane < 16 ? tok + lane : tok - 1;
+  const int s_at = lane <= 16 && idx >= 0 && idx < T ? slots[idx] : -1;
+  const int slot = __shfl_sync(0xffffffffu, s_at, 0), prev = __shfl_sync(0xffffffffu, s_at, 16);
+  if (slot < 0) return;
+  if (slot >= num_pages * kPage) {
+    if (lane == 0 && dev_status) atomicOr(dev_status, 0x4 /*PKV_DEV_BAD_SLOT*/);
+    return;
+  }
+  const int page = slot / kPage, off = slot % kPage;
+  if (prev >= 0 && prev / kPage == page) {
+    // not a leader; out of order it belongs to no run
+    if (prev + 1 != slot && lane == 0 && dev_status) atomicOr(dev_status, 0x4);
+    return;
+  }
+  // the run: tokens tok .. tok + n - 1 at offsets off .. off + n - 1
+  const unsigned follow = __ballot_sync(0xffffffffu, lane < 16 && lane + off < kPage && s_at == slot + lane);
+  const int n = __ffs(~follow) - 1;
+  const size_t blk = static_cast<size_t>(page) * Hkv + h;
+  uint8_t* const block = (which ? v_cache : k_cache) + blk * kPage * D;
+  float* const scale = (which ? v_scale : k_scale) + blk;
+  const void* const src = which ? v_new : k_new;
+
+  // old block (only where bytes of it may stay: rows before the run; V also rows behind it):
+  // K 16-byte pieces lane + 32 i, V the 16 token bytes of head-dim rows lane * E + i
+  const bool old_rows = off > 0, fetch = which ? n < kPage : old_rows;
+  float s_old = old_rows ? *scale : 0.f;
+  uint4 was[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i)
+    was[i] = fetch ? reinterpret_cast<const uint4*>(block)[which ? lane * E + i : lane + 32 * i]
+                   : make_uint4(0u, 0u, 0u, 0u);
+  float x[kPage][E];  // the token at page offset t, elements lane * E ..
+  float amax = 0.f;
+#pragma unroll
+  for (int t = 0; t < kPage; ++t) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[t][e] = 0.f;
+    if (t >= off && t < off + n) {
+      const size_t at = (static_cast<size_t>(tok + t - off) * Hkv + h) * D + lane * E;
+      if constexpr (NEW_DT == kBF16) {
+        const uint32_t* p = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(src) + at);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const uint32_t v = p[e / 2];
+          x[t][e] = __uint_as_float(v << 16);
+          x[t][e + 1] = __uint_as_float(v & 0xffff0000u);
+        }
+      } else {
+        const float2* p = reinterpret_cast<const float2*>(static_cast<const float*>(src) + at);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 v = p[e / 2];
+          x[t][e] = v.x;
+          x[t][e + 1] = v.y;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < kPage; ++t)
+#pragma unroll
+    for (int e = 0; e < E; ++e) amax = fmaxf(amax, fabsf(x[t][e]));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const float need = block_scale<FP8>(amax);
+  const float s = old_rows ? fmaxf(s_old, need) : need;
+  const bool again = old_rows && s > s_old;
+  const float by = again ? __fdiv_rn(s_old, s) : 1.f;
+  if (lane == 0) *scale = s;
+
+  if (which == 0) {  // K: a row of D bytes per token
+    if (again) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        if ((lane + 32 * i) * 16 / D >= off) continue;
+        uint32_t w[4] = {was[i].x, was[i].y, was[i].z, was[i].w};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint32_t m = 0;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) m |= block_recode<FP8>((w[u] >> (8 * b)) & 0xffu, by) << (8 * b);
+          w[u] = m;
+        }
+        reinterpret_cast<uint4*>(block)[lane + 32 * i] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kPage; ++t) {
+      if (t < off || t >= off + n) continue;
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) m |= block_code<FP8>(x[t][e], s) << (8 * e);
+      uint8_t* const row = block + t * D + lane * E;
+      if constexpr (E == 4) *reinterpret_cast<uint32_t*>(row) = m;
+      else *reinterpret_cast<uint16_t*>(row) = static_cast<uint16_t>(m);
+    }
+  } else {  // V: 16 token bytes per head-dim row; the lane's rows are lane * E ..
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const uint32_t w[4] = {was[i].x, was[i].y, was[i].z, was[i].w};
+      uint32_t out[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int t = 4 * u + b;
+          uint32_t byte = (w[u] >> (8 * b)) & 0xffu;
+          if (t < off) {
+            if (again) byte = block_recode<FP8>(byte, by);
+          } else if (t < off + n) {
+            byte = block_code<FP8>(x[t][i], s);
+          }
+          m |= byte << (8 * b);
+        }
+        out[u] = m;
+      }
+      reinterpret_cast<uint4*>(block)[lane * E + i] = make_uint4(out[0], out[1], out[2], out[3]);
+    }
+  }
+}
+
+template <bool FP8>
+cudaError_t launch_block(const CacheView& c, void* k, void* v, float* ks, float* vs, const void* kn,
+                         const void* vn, int new_dtype, const int32_t* slots, int T,
+                         int32_t* dev_status, cudaStream_t st) {
+  const long long items = 2ll * T * c.Hkv;
+  const dim3 grid(static_cast<unsigned>((items + kWarps - 1) / kWarps));
+  uint8_t* kb = static_cast<uint8_t*>(k);
+  uint8_t* vb = static_cast<uint8_t*>(v);
+  const bool nb = new_dtype == kBF16;
+#define PKV_BLOCK(ND, DD)                                                                      \
+  append_block_kernel<FP8, ND, DD><<<grid, kWarps * 32, 0, st>>>(kb, vb, ks, vs, kn, vn, slots, \
+                                                                 T, c.Hkv, c.num_pages, dev_status)
+  if (c.D == 64) {
+    if (nb) PKV_BLOCK(kBF16, 64);
+    else PKV_BLOCK(kF32, 64);
+  } else {
+    if (nb) PKV_BLOCK(kBF16, 128);
+    else PKV_BLOCK(kF32, 128);
+  }
+#undef PKV_BLOCK
+  return cudaGetLastError();
+}
+
 template <int KV_DT, int NEW_DT>
 cudaError_t launch_t(int D, dim3 grid, cudaStream_t st, void* k, void* v, float* ks,
                      float* vs, const void* kn, const void* vn, const int32_t* slots, int T,
@@ -162,6 +334,12 @@ cudaError_t launch_append(const CacheView& c, void* k_cache, void* v_cache, floa
                                          slots, T, c.Hkv, c.num_pages, dev_status)
                 : launch_t<kINT4, kF32>(c.D, grid, st, k_cache, v_cache, ks, vs, k_new, v_new,
                                         slots, T, c.Hkv, c.num_pages, dev_status);
+    case kINT8B:
+      return launch_block<false>(c, k_cache, v_cache, ks, vs, k_new, v_new, new_dtype, slots, T,
+                                 dev_status, st);
+    case kFP8B:
+      return launch_block<true>(c, k_cache, v_cache, ks, vs, k_new, v_new, new_dtype, slots, T,
+                                dev_status, st);
     default:
       return cudaErrorInvalidValue;
   }

@@ -131,7 +131,8 @@ template <int KVT, int D>
 struct Layout {
   static constexpr int kBytes = kPage * RowBytes<KVT, D>::value;   // K block of one (page, head)
   static constexpr int vBytes = kBytes;                            // V block of one (page, head)
-  static constexpr int sBytes = quantised(KVT) ? kPage * 4 : 0;  // one scale vector
+  // one scale vector; the block-scaled formats have one K and one V scale in 16 bytes
+  static constexpr int sBytes = block_scaled(KVT) ? 8 : quantised(KVT) ? kPage * 4 : 0;
   static constexpr int pageBytes = kBytes + vBytes + 2 * sBytes;
   static constexpr int S = Tune<KVT, D>::S;
   static constexpr int stageBytes = pageBytes;
@@ -207,6 +208,14 @@ __device__ __forceinline__ void split_b2(float a, float b, uint32_t& hi, uint32_
 __device__ __forceinline__ void u8x4_to_f16x4_biased(uint32_t w, uint32_t& lo, uint32_t& hi) {
   asm("prmt.b32 %0, %1, %2, 0x4140;" : "=r"(lo) : "r"(w), "r"(0x64646464u));
   asm("prmt.b32 %0, %1, %2, 0x4342;" : "=r"(hi) : "r"(w), "r"(0x64646464u));
+}
+
+// The same bytes -> the codes themselves, exactly: 1152 is taken off in f16.
+__device__ __forceinline__ void u8x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  uint32_t a, b;
+  u8x4_to_f16x4_biased(w, a, b);
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
 }
 
 // Four E4M3 codes (a 32-bit word) -> two f16x2 words holding their exact values (every
@@ -602,6 +611,10 @@ struct QuantWarp {
   float2 nm2, rs2;
   float2 l2, sp2;  // running sums of P and of P * s_v, two partial sums each
   float kbias;     // kBias * sum(q) of the head, as the MMA sees q
+  // Block-scaled formats: a power of two that brings the V scales up to about 2^5, so that
+  // the f16 remainder of P * s_v keeps its bits: at scales near 2^-6 and probabilities near
+  // 2^-6 the remainders were subnormal, and a 32k context came out 1.0e-5 off in the mean.
+  float vgain;
 
   // k-slot pair {2c, 2c+1} of k-step ks <-> head_dim 64(ks/4) + 16c + 4(ks%4): each lane's
   // K operand is then one contiguous 16-byte shared-memory load per n-tile.
@@ -702,11 +715,14 @@ struct QuantWarp {
       qsum += __shfl_xor_sync(0xffffffffu, qsum, 2);
       if (c == 0) {
         rowc[r] = ldexpf(p.scale_log2, e - kMulLog2);
+        // (never 0: a masked score of -inf has to stay -inf)
+        if constexpr (block_scaled(KVT)) rowc[r] = fmaxf(rowc[r], 1e-37f);
         rowc[kMaxHeads + r] = ldexpf(kBias, kMulLog2) * qsum;  // K entered as 2^m (kBias + code)
       }
     }
     nm2 = make_float2(CUDART_INF_F, CUDART_INF_F);
     l2 = sp2 = make_float2(0.f, 0.f);
+    vgain = 1.2676506e30f;  // 2^100: the first page brings it down
 #pragma unroll
     for (int j = 0; j < MT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
     (void)b; (void)h0;
@@ -721,7 +737,7 @@ struct QuantWarp {
     rs2 = make_float2(rs, rs);
     kbias = rowc[kMaxHeads + r];
     a_q = smem_u32(aux) + lane * 16;
-    a_sc = stage0 + 2 * Lo::kBytes + c * 16;
+    a_sc = stage0 + 2 * Lo::kBytes + (block_scaled(KVT) ? 0 : c * 16);
     // K rows of n-tile 0: token 4(r/2) + r%2 (n-tile 1: two tokens further)
     a_k = stage0 + (4 * (r >> 1) + (r & 1)) * RB + c * (KVT == kINT4 ? 8 : 16);
     a_v = stage0 + Lo::kBytes + lane * 16;
@@ -731,7 +747,7 @@ struct QuantWarp {
   // score -inf and V scale 0; FP8 V codes of those tokens are also set to zero in shared
   // memory, because a stale E4M3 NaN code would survive a zero probability in the MMA.
   __device__ void mask_v_codes(uint32_t so, int valid, int lo, int lane) {
-    if constexpr (KVT == kFP8) {
+    if constexpr (KVT == kFP8 || KVT == kFP8B) {
       using Lo = Layout<KVT, D>;
       // V block: D rows of 16 token bytes; keep bytes t with lo <= t < valid
       const uint32_t keep_lo = (valid >= 16 ? 0xffffu : ((1u << valid) - 1u)) & ~((1u << lo) - 1u);
@@ -758,8 +774,10 @@ struct QuantWarp {
 
   // Two B operands (k-slot pairs of one k-step) of a 32-bit word of stored K codes.
   __device__ static void kcvt(uint32_t w, int half, uint32_t& b0, uint32_t& b1) {
-    if constexpr (KVT == kFP8) {
+    if constexpr (KVT == kFP8 || KVT == kFP8B) {
       e4m3x4_to_f16x4(w, b0, b1);
+    } else if constexpr (KVT == kINT8B) {
+      u8x4_to_f16x4(w, b0, b1);
     } else if constexpr (KVT == kINT8) {
       u8x4_to_f16x4_biased(w, b0, b1);
     } else {  // INT4: elements (2 half, 2 half + 4) and (2 half + 1, 2 half + 5) of the word
@@ -771,8 +789,27 @@ struct QuantWarp {
   // not attended (the ragged last page, or the page holding a window's first key).
   __device__ __forceinline__ void page(uint32_t so, bool partial, int valid, int lo, int lane) {
     const int c = lane & 3;
-    const float4 k4 = lds_f4(a_sc + so);
-    float4 v4 = lds_f4(a_sc + so + kPage * 4);
+    float4 k4, v4;
+    if constexpr (block_scaled(KVT)) {  // the page's K and V scale
+      const uint2 s = lds_u2(a_sc + so);
+      k4.x = k4.y = k4.z = k4.w = __uint_as_float(s.x);
+      float vg = __uint_as_float(s.y) * vgain;
+      if (vg > 128.f) {  // (the same for the whole warp; P <= 2^8 keeps the product in f16)
+        const int e = 259 - static_cast<int>((s.y >> 23) & 0xffu);  // 2^(5 - exponent of s_v)
+        const float g = __uint_as_float(static_cast<uint32_t>(min(max(e, 1), 254)) << 23);
+        const float by = g / vgain;
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
+          o[j][0] *= by; o[j][1] *= by; o[j][2] *= by; o[j][3] *= by;
+        }
+        vgain = g;
+        vg = __uint_as_float(s.y) * g;
+      }
+      v4.x = v4.y = v4.z = v4.w = vg;
+    } else {
+      k4 = lds_f4(a_sc + so);
+      v4 = lds_f4(a_sc + so + kPage * 4);
+    }
     // S = Q K^T over the page's 16 tokens: n-tile j column n holds token
     // 4(n/2) + 2j + (n%2), so lane (r, c) ends up with tokens 4c .. 4c+3 of head r.  The
     // accumulators of the hi rows start at -kbias: the code bias cancels in FP32.
@@ -799,7 +836,10 @@ struct QuantWarp {
         uint32_t b0, b1, b2, b3;
         kcvt(kw0[wi], s & 1, b0, b1);
         kcvt(kw1[wi], s & 1, b2, b3);
-        if (blk == 0 && s == 0) {
+        if (block_scaled(KVT) && blk == 0 && s == 0) {  // exact codes: no bias
+          mma_f16_c(s0, a, b0, b1, 0.f, 0.f, 0.f, 0.f);
+          mma_f16_c(s1, a, b2, b3, 0.f, 0.f, 0.f, 0.f);
+        } else if (blk == 0 && s == 0) {
           mma_f16_c(s0, a, b0, b1, -kbias, -kbias, 0.f, 0.f);
           mma_f16_c(s1, a, b2, b3, -kbias, -kbias, 0.f, 0.f);
         } else {
@@ -851,7 +891,7 @@ struct QuantWarp {
     l2 = __fadd2_rn(l2, __fadd2_rn(p01, p23));
     const float2 pv01 = __fmul2_rn(p01, make_float2(v4.x, v4.y));
     const float2 pv23 = __fmul2_rn(p23, make_float2(v4.z, v4.w));
-    sp2 = __fadd2_rn(sp2, __fadd2_rn(pv01, pv23));
+    if constexpr (!block_scaled(KVT)) sp2 = __fadd2_rn(sp2, __fadd2_rn(pv01, pv23));
     // B = P^T (tokens x heads): lane (r, c) holds head r, tokens 4c .. 4c+3, which the
     // k-slot order {2c, 2c+1 | 2c+8, 2c+9} -> tokens {4c, 4c+1 | 4c+2, 4c+3} makes a
     // ready-made fragment (INT4: {4c, 4c+2 | 4c+1, 4c+3}, the order in which its V bytes
@@ -882,9 +922,12 @@ struct QuantWarp {
         // low nibbles row 16 j + r, high nibbles row 16 j + r + 8
         e2m3x4_to_f16x4(s4x4_to_e2m3x4<0>(w[j]), a[0], a[2]);
         e2m3x4_to_f16x4(s4x4_to_e2m3x4<1>(w[j]), a[1], a[3]);
-      } else if constexpr (KVT == kFP8) {
+      } else if constexpr (KVT == kFP8 || KVT == kFP8B) {
         e4m3x4_to_f16x4(w[2 * j], a[0], a[2]);
         e4m3x4_to_f16x4(w[2 * j + 1], a[1], a[3]);
+      } else if constexpr (KVT == kINT8B) {
+        u8x4_to_f16x4(w[2 * j], a[0], a[2]);
+        u8x4_to_f16x4(w[2 * j + 1], a[1], a[3]);
       } else {
         u8x4_to_f16x4_biased(w[2 * j], a[0], a[2]);
         u8x4_to_f16x4_biased(w[2 * j + 1], a[1], a[3]);
@@ -908,9 +951,13 @@ struct QuantWarp {
     // V entered the MMA as 2^m (kBias + code) against P s_v: remove 2^m kBias sum(P s_v)
     // of heads 2c and 2c + 1, then the factor 2^m (once here rather than on every page's
     // V scales)
-    constexpr float vb = kBias * kUnit, up = 1.f / kUnit;
-    const float ba = vb * __shfl_sync(0xffffffffu, st, 8 * c);
-    const float bb = vb * __shfl_sync(0xffffffffu, st, 8 * c + 4);
+    constexpr float vb = kBias * kUnit;
+    const float up = block_scaled(KVT) ? 1.f / vgain : 1.f / kUnit;
+    float ba = 0.f, bb = 0.f;
+    if constexpr (!block_scaled(KVT)) {
+      ba = vb * __shfl_sync(0xffffffffu, st, 8 * c);
+      bb = vb * __shfl_sync(0xffffffffu, st, 8 * c + 4);
+    }
     float* oa = cO + (2 * c) * (D + 2);
     float* ob = oa + (D + 2);
 #pragma unroll
@@ -944,6 +991,14 @@ struct WarpOf<kFP8, D> {
 template <int D>
 struct WarpOf<kINT4, D> {
   using type = QuantWarp<kINT4, D>;
+};
+template <int D>
+struct WarpOf<kINT8B, D> {
+  using type = QuantWarp<kINT8B, D>;
+};
+template <int D>
+struct WarpOf<kFP8B, D> {
+  using type = QuantWarp<kFP8B, D>;
 };
 
 // ------------------------------------------------------------------ the kernel
@@ -1168,7 +1223,8 @@ __global__ void __launch_bounds__(Tune<KVT, D>::W * 32, Tune<KVT, D>::minBlocks)
   // bulk-copy engine then handles two copies per page instead of four (at the start of a
   // launch, 28 warps of an SM request 3 stages each at once).  The lane's source base,
   // page stride and destination are computed once.
-  constexpr int kScaleLanes = quantised(KVT) ? 8 : 0;
+  // (block-scaled formats: lanes 8 and 9 copy the page's K and V scale, 4 bytes each)
+  constexpr int kScaleLanes = block_scaled(KVT) ? 2 : quantised(KVT) ? 8 : 0;
   const int ck = lane < 2 ? lane : 0;
   constexpr uint32_t c_bytes = static_cast<uint32_t>(Lo::kBytes);
   const uint32_t c_dst = smem_u32(my_stages) + (ck == 0 ? 0u : c_bytes);
@@ -1177,9 +1233,14 @@ __global__ void __launch_bounds__(Tune<KVT, D>::W * 32, Tune<KVT, D>::minBlocks)
   const int sl = lane - 8;  // scale lanes: sl / 4 = K or V vector, sl % 4 = 16-byte piece
   const bool s_lane = kScaleLanes > 0 && sl >= 0 && sl < kScaleLanes;
   const uint32_t s_dst = smem_u32(my_stages) + 2 * c_bytes +
-                         (s_lane ? static_cast<uint32_t>((sl >> 2) * Lo::sBytes + (sl & 3) * 16) : 0u);
-  const float* s_src = s_lane ? (sl >> 2 ? p.vs : p.ks) + static_cast<size_t>(g) * kPage + (sl & 3) * 4 : nullptr;
-  const size_t s_stride = static_cast<size_t>(p.Hkv) * kPage;  // floats from one page to the next
+                         (!s_lane             ? 0u
+                          : block_scaled(KVT) ? static_cast<uint32_t>(sl * 4)
+                                              : static_cast<uint32_t>((sl >> 2) * Lo::sBytes + (sl & 3) * 16));
+  const float* s_src = !s_lane             ? nullptr
+                       : block_scaled(KVT) ? (sl ? p.vs : p.ks) + g
+                                           : (sl >> 2 ? p.vs : p.ks) + static_cast<size_t>(g) * kPage + (sl & 3) * 4;
+  // floats from one page to the next
+  const size_t s_stride = static_cast<size_t>(p.Hkv) * (block_scaled(KVT) ? 1 : kPage);
   const uint32_t bar0 = smem_u32(my_bars);
   const uint64_t pol = l2_evict_first_policy();  // streamed once: keep L2 for others
   auto issue = [&](int i, int stage) {
@@ -1189,8 +1250,12 @@ __global__ void __launch_bounds__(Tune<KVT, D>::W * 32, Tune<KVT, D>::minBlocks)
     bulk_g2s_if(lane < 2, c_dst + stage * Lo::stageBytes, c_src + static_cast<size_t>(pid) * c_stride,
                 c_bytes, bar, pol);
     if (s_lane) {
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s_dst + stage * Lo::stageBytes),
-                   "l"(s_src + static_cast<size_t>(pid) * s_stride) : "memory");
+      if constexpr (block_scaled(KVT))
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s_dst + stage * Lo::stageBytes),
+                     "l"(s_src + static_cast<size_t>(pid) * s_stride) : "memory");
+      else
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(s_dst + stage * Lo::stageBytes),
+                     "l"(s_src + static_cast<size_t>(pid) * s_stride) : "memory");
       asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
     }
   };
@@ -1710,8 +1775,9 @@ constexpr int max_splits_of() {
   {kernel_ptr<T, D, ST, WN>(), Smem<T, D, ST>::total, I, max_splits_of<T, D>(), \
    Tune<T, D>::W}
 // index: dtype-and-head-dim slot (0 .. 9), + 10 for the fused decode step, + 20 for the
-// sliding window
-constexpr int kVariants = 40;
+// sliding window; 40 .. 47 the block-scaled formats (no fused step: a new row can change
+// its whole block's codes)
+constexpr int kVariants = 48;
 Variant variant(int dtype, int D, bool step, bool win) {
   switch (dtype * 1000 + D + (step ? 100000 : 0) + (win ? 1000000 : 0)) {
 #define PKV_VARIANTS_OF(ST, WN, BASE, KEY)                                                \
@@ -1729,6 +1795,14 @@ Variant variant(int dtype, int D, bool step, bool win) {
     PKV_VARIANTS_OF(true, false, 10, 100000)
     PKV_VARIANTS_OF(false, true, 20, 1000000)
     PKV_VARIANTS_OF(true, true, 30, 1100000)
+#undef PKV_VARIANTS_OF
+#define PKV_VARIANTS_OF(WN, BASE, KEY)                                                    \
+    case KEY + kINT8B * 1000 + 64: return PKV_VARIANT(kINT8B, 64, false, WN, BASE + 0);   \
+    case KEY + kINT8B * 1000 + 128: return PKV_VARIANT(kINT8B, 128, false, WN, BASE + 1); \
+    case KEY + kFP8B * 1000 + 64: return PKV_VARIANT(kFP8B, 64, false, WN, BASE + 2);     \
+    case KEY + kFP8B * 1000 + 128: return PKV_VARIANT(kFP8B, 128, false, WN, BASE + 3);
+    PKV_VARIANTS_OF(false, 40, 0)
+    PKV_VARIANTS_OF(true, 44, 1000000)
 #undef PKV_VARIANTS_OF
     default: return {nullptr, 0, -1, 1, 4};
   }

@@ -8,11 +8,13 @@ namespace pkv {
 
 constexpr int kPage = 16;  // tokens per page (the only supported page size)
 
-enum : int { kF32 = 0, kBF16 = 1, kINT8 = 2, kFP8 = 3, kINT4 = 4 };
+enum : int { kF32 = 0, kBF16 = 1, kINT8 = 2, kFP8 = 3, kINT4 = 4, kINT8B = 5, kFP8B = 6 };
 
-// Formats stored as codes with one FP32 scale per (token, kv head).
+// 8-bit formats with one FP32 scale per (page, kv head): a block of kPage tokens.
+__host__ __device__ constexpr bool block_scaled(int dtype) { return dtype == kINT8B || dtype == kFP8B; }
+// Formats stored as codes with FP32 scales (one per (token, kv head) or one per block).
 __host__ __device__ constexpr bool quantised(int dtype) {
-  return dtype == kINT8 || dtype == kFP8 || dtype == kINT4;
+  return dtype == kINT8 || dtype == kFP8 || dtype == kINT4 || block_scaled(dtype);
 }
 
 // BF16 page blocks are stored as tensor-core tiles: 8 x 8 "core matrices" of 16-byte
@@ -114,5 +116,7 @@ cudaError_t launch_prefill(const PrefillArgs& a, const PrefillPlan& plan, cudaSt
 int prefill_tc_rows();
 int prefill_tc_blocks_per_sm(int q_dtype);
 cudaError_t launch_prefill_tc(const PrefillArgs& a, int n_row_tiles, int ksplit, cudaStream_t st);
+// The same over a block-scaled 8-bit cache.
+cudaError_t launch_prefill_blk(const PrefillArgs& a, int n_row_tiles, int ksplit, cudaStream_t st);
 
 }  // namespace pkv

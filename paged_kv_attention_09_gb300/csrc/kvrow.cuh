@@ -69,6 +69,46 @@ __device__ __forceinline__ float quantize_row_fp8(const float (&x)[E], uint8_t (
   return s;
 }
 
+// ---- block-scaled 8-bit formats: one scale for the 16 tokens of a (page, kv head)
+// INT8B: s = max|x| / 127 (IEEE division), code = clamp(rint(x / s), -127, 127), stored as
+// INT8 bytes.  FP8B: s = 2^e, the smallest with max|x| / s <= 448 (e >= -126), code = E4M3 of
+// x / s: dividing by a power of two is exact, so re-coding at a grown scale loses only bits
+// that leave the E4M3 range, and a block that grows several times stays as good as one coded
+// at once.  (448 = 1.75 * 2^8: e is max|x|'s exponent less 8, plus one above 1.75.)
+template <bool FP8>
+__device__ __forceinline__ float block_scale(float amax) {
+  if constexpr (!FP8) {
+    return __fdiv_rn(amax, 127.0f);
+  } else {
+    if (amax == 0.f) return 0.f;
+    const uint32_t u = __float_as_uint(amax);
+    const int e = static_cast<int>(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return __uint_as_float(static_cast<uint32_t>(e < 1 ? 1 : e) << 23);
+  }
+}
+// The stored byte of x at scale s (0 when the block is all zero).
+template <bool FP8>
+__device__ __forceinline__ uint32_t block_code(float x, float s) {
+  if constexpr (!FP8) {
+    float r = 0.f;
+    if (s != 0.f) r = fminf(fmaxf(rintf(__fdiv_rn(x, s)), -127.f), 127.f);
+    return static_cast<uint32_t>(static_cast<int>(r) + 128);
+  } else {
+    return s != 0.f ? __nv_cvt_float_to_fp8(__fdiv_rn(x, s), __NV_SATFINITE, __NV_E4M3) : 0u;
+  }
+}
+// A stored byte coded again at a scale 1 / by times as large (by = old scale / new, < 1).
+template <bool FP8>
+__device__ __forceinline__ uint32_t block_recode(uint32_t byte, float by) {
+  if constexpr (!FP8) {
+    const float c = static_cast<float>(static_cast<int>(byte) - 128);
+    return static_cast<uint32_t>(static_cast<int>(rintf(c * by)) + 128);
+  } else {
+    const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte), __NV_E4M3);
+    return __nv_cvt_float_to_fp8(__half2float(__half(h)) * by, __NV_SATFINITE, __NV_E4M3);
+  }
+}
+
 // ---- INT4 storage (two 4-bit two's-complement codes per byte)
 // K rows: every 8 consecutive head-dim elements form a little-endian 32-bit word; element
 // e of the word sits at bit 4 * ((e >> 1) + 4 * (e & 1)) (even elements in the low half).

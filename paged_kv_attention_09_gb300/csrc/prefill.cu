@@ -1,4 +1,5 @@
-// prefill.cu — planning of chunked-prefill attention over a paged BF16 KV cache.
+// prefill.cu — planning of chunked-prefill attention over a paged KV cache (BF16 or
+// block-scaled 8-bit).
 //
 // Sources: "Tiny-LLM-Inference Project_Status" (chunked prefill/decode scheduling; the
 // chunked-prefill SDPA path; dedicated BF16 paged-attention kernel) and "tinyloop
@@ -8,7 +9,7 @@
 //
 // The rows of a launch are (chunk token, query head) pairs of one GQA group, token-major
 // (row = i * G + head), so the query heads that share a kv head share every K/V tile;
-// the tcgen05 kernel (prefill_tc.cu) takes them in tiles of 128.
+// the tcgen05 kernels (prefill_tc.cu, prefill_blk.cu) take them in tiles of 128.
 #include <mutex>
 
 #include "internal.h"
@@ -34,7 +35,7 @@ int sm_count(int device) {
 bool plan_prefill(const CacheView& c, int B, int Hq, int max_q_len, int MB, int q_dtype,
                   int device, const PrefillOpts& opts, PrefillPlan* plan) {
   (void)MB;
-  if (c.dtype != kBF16) return false;
+  if (c.dtype != kBF16 && !block_scaled(c.dtype)) return false;
   if (c.D != 64 && c.D != 128) return false;
   const int G = Hq / c.Hkv;
   plan->rows_per_cta = prefill_tc_rows();
@@ -66,6 +67,7 @@ bool plan_prefill(const CacheView& c, int B, int Hq, int max_q_len, int MB, int 
 }
 
 cudaError_t launch_prefill(const PrefillArgs& a, const PrefillPlan& plan, cudaStream_t st) {
+  if (block_scaled(a.c.dtype)) return launch_prefill_blk(a, plan.n_row_tiles, plan.ksplit, st);
   return launch_prefill_tc(a, plan.n_row_tiles, plan.ksplit, st);
 }
 

@@ -14,15 +14,18 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libpkv.so")
 
-F32, BF16, INT8, FP8, INT4 = 0, 1, 2, 3, 4
-CODED = (INT8, FP8, INT4)  # stored as codes with one FP32 scale per (token, kv head)
+F32, BF16, INT8, FP8, INT4, INT8B, FP8B = 0, 1, 2, 3, 4, 5, 6
+BLOCK_SCALED = (INT8B, FP8B)  # 8-bit codes with one FP32 scale per (page, kv head)
+# stored as codes with one FP32 scale per (token, kv head), or per block of a page's tokens
+CODED = (INT8, FP8, INT4) + BLOCK_SCALED
 # element containers of the cache tensors (FP8 codes and INT4 code pairs as raw bytes)
 # (INT8 bytes hold code + 128, offset binary)
 _TORCH_DTYPE = {F32: torch.float32, BF16: torch.bfloat16, INT8: torch.uint8, FP8: torch.uint8,
-                INT4: torch.uint8}
+                INT4: torch.uint8, INT8B: torch.uint8, FP8B: torch.uint8}
 _CODE = {torch.float32: F32, torch.bfloat16: BF16}
 
 DEV_BAD_PAGE, DEV_BAD_LEN, DEV_BAD_SLOT, DEV_BAD_CHUNK, DEV_TIMEOUT = 0x1, 0x2, 0x4, 0x8, 0x10
+DEV_NO_PAGES = 0x20
 STATUS = {0: "PKV_OK", 1: "PKV_ERR_NULL", 2: "PKV_ERR_SHAPE", 3: "PKV_ERR_DTYPE",
           4: "PKV_ERR_PAGE_SIZE", 5: "PKV_ERR_ALIGN", 6: "PKV_ERR_WORKSPACE",
           7: "PKV_ERR_UNSUPPORTED", 8: "PKV_ERR_LAUNCH", 9: "PKV_ERR_DEVICE"}
@@ -32,7 +35,8 @@ EXPORTS = ("pkv_append", "pkv_decode_workspace_size", "pkv_decode_attn", "pkv_de
            "pkv_prefill_workspace_size_ex", "pkv_prefill_chunk_attn_ex",
            "pkv_decode_attn_noalloc", "pkv_decode_attn_noalloc_ex", "pkv_status_string",
            "pkv_decode_graph_workspace_size", "pkv_decode_graph_create",
-           "pkv_decode_graph_launch", "pkv_decode_graph_bucket", "pkv_decode_graph_destroy")
+           "pkv_decode_graph_launch", "pkv_decode_graph_bucket", "pkv_decode_graph_destroy",
+           "pkv_batch_tables", "pkv_rope_plan_init", "pkv_rope")
 GRAPH_MAX_BUCKETS = 16
 NOALLOC_SCRATCH_BYTES = 4 << 20
 
@@ -74,6 +78,30 @@ class pkv_decode_graph_desc(ctypes.Structure):
                 ("scale", ctypes.c_float), ("workspace", ctypes.c_void_p),
                 ("workspace_bytes", ctypes.c_size_t), ("dev_status", ctypes.c_void_p),
                 ("num_buckets", ctypes.c_int32), ("buckets", ctypes.POINTER(ctypes.c_int32))]
+
+
+class pkv_page_pool(ctypes.Structure):
+    _fields_ = [("ring", ctypes.c_void_p), ("state", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
+ROPE_MAX_PAIRS = 128
+ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+ROPE_SCALING = {"none": 0, "linear": 1, "base": 2, "bands": 3}
+
+
+class pkv_rope_params(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("transposed", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("theta", ctypes.c_double), ("factor", ctypes.c_double),
+                ("low", ctypes.c_double), ("high", ctypes.c_double),
+                ("original_len", ctypes.c_int32), ("attention_factor", ctypes.c_float)]
+
+
+class pkv_rope_plan(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("transposed", ctypes.c_int32), ("attention_factor", ctypes.c_float),
+                ("freq", ctypes.c_uint64 * ROPE_MAX_PAIRS)]
 
 
 _lib = None
@@ -124,6 +152,15 @@ def bind(path: str):
     lib.pkv_decode_attn_noalloc_ex.restype = ctypes.c_int
     lib.pkv_status_string.argtypes = [ctypes.c_int]
     lib.pkv_status_string.restype = ctypes.c_char_p
+    I64 = ctypes.c_int64
+    lib.pkv_batch_tables.argtypes = [ctypes.POINTER(pkv_page_pool), P, P, I32, P, I32, P, P, P, P,
+                                     I32, P, P]
+    lib.pkv_rope_plan_init.argtypes = [ctypes.POINTER(pkv_rope_params),
+                                       ctypes.POINTER(pkv_rope_plan)]
+    lib.pkv_rope.argtypes = [ctypes.POINTER(pkv_rope_plan), P, P, I64, I64, I32, P, P, I64, I64,
+                             I32, I32, I32, I32, P, P]
+    for fn in ("pkv_batch_tables", "pkv_rope_plan_init", "pkv_rope"):
+        getattr(lib, fn).restype = ctypes.c_int
     GD = ctypes.POINTER(pkv_decode_graph_desc)
     lib.pkv_decode_graph_workspace_size.argtypes = [GD, ctypes.POINTER(SZ)]
     lib.pkv_decode_graph_create.argtypes = [GD, ctypes.POINTER(ctypes.c_void_p)]
@@ -184,7 +221,8 @@ class KVCache:
     """Device tensors of one paged cache in the library's layout.
 
     k: [num_pages, Hkv, 16, D]; v: [num_pages, Hkv, D, 16] (page blocks transposed);
-    k_scale, v_scale: float32 [num_pages, Hkv, 16] for INT8, FP8 and INT4 caches.  For
+    k_scale, v_scale: float32 [num_pages, Hkv, 16] for INT8, FP8 and INT4 caches,
+    [num_pages, Hkv] for INT8B and FP8B.  For
     BF16 caches the elements inside each (page, kv head) block are in tensor-core tile
     order, FP8 codes are bytes, and INT4 blocks hold two codes per byte (k: [.., 16, D/2],
     v: [.., D/2, 16] bytes); see include/pkv.h.  The tensor shapes are containers of the
@@ -211,7 +249,8 @@ class KVCache:
             v = torch.zeros(num_pages, num_kv_heads, head_dim, page_size, dtype=dt, device=device)
         ks = vs = None
         if kv_dtype in CODED:
-            ks = torch.zeros(num_pages, num_kv_heads, page_size, dtype=torch.float32, device=device)
+            per = () if kv_dtype in BLOCK_SCALED else (page_size,)
+            ks = torch.zeros(num_pages, num_kv_heads, *per, dtype=torch.float32, device=device)
             vs = torch.zeros_like(ks)
         return cls(k, v, ks, vs, kv_dtype=kv_dtype)
 
@@ -425,6 +464,170 @@ def pkv_prefill_chunk_attn(cache: KVCache, q: torch.Tensor, q_start_loc: torch.T
                   _ptr(context_lens), float(scale), _ptr(out), _ptr(workspace), wb,
                   _prefill_opts(key_split), _ptr(dev_status), _stream(stream)),
                  "pkv_prefill_chunk_attn", bound)
+
+
+class PagePool:
+    """A pool of page ids on the GPU, from which pkv_batch_tables takes the new pages of a
+    step and to which it returns those of ended requests (see include/pkv.h).
+
+    ring: int32 [num_pages]; state: int32 [4], the first free entry and their number."""
+
+    def __init__(self, ring: torch.Tensor, state: torch.Tensor, page_size: int = 16):
+        _int32("ring", ring, 1)
+        _int32("state", state, 1, ring.device)
+        if state.numel() < 4:
+            raise ValueError("state: int32 [4] is wanted")
+        self.ring, self.state, self.index = ring, state, ring.get_device()
+        self._struct = pkv_page_pool(ring.data_ptr(), state.data_ptr(), ring.numel(), page_size)
+        self._ref = ctypes.byref(self._struct)
+
+    @classmethod
+    def allocate(cls, num_pages: int, device="cuda") -> "PagePool":
+        """A pool with all its pages free."""
+        return cls(torch.arange(num_pages, dtype=torch.int32, device=device),
+                   torch.tensor([0, num_pages, 0, 0], dtype=torch.int32, device=device))
+
+
+def _int32(name: str, t: torch.Tensor, dims: int, device=None) -> None:
+    if t.dtype is not torch.int32 or t.dim() != dims or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous int32 tensor of {dims} dimension(s) is wanted, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _is_int32(t: torch.Tensor, shape: tuple, index: int) -> bool:
+    """A contiguous int32 tensor of this shape on this device (get_device's number)."""
+    return t.dtype is torch.int32 and t.shape == shape and t.is_contiguous() and \
+        t.get_device() == index
+
+
+def _issue(fn, args, what: str, bound: bool, index: int):
+    """_call with the tensors' device current (a bound call is issued as the caller's
+    current device stands: bind and issue it there).  index: the device's number, -1: CPU."""
+    if bound:
+        return BoundCall(fn, args, what)
+    if index >= 0 and index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            code = fn(*args)
+    else:
+        code = fn(*args)
+    if code != 0:
+        raise PkvError(code, what)
+    return None
+
+
+# the current stream's handle without building a Stream object (a microsecond or two per
+# call), where this torch offers it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(stream, index: int) -> int:
+    """The stream argument: given, or the current stream of the tensors' device."""
+    if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(index)
+        return torch.cuda.current_stream(index).cuda_stream
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def pkv_batch_tables(pool: PagePool, cached_lens: torch.Tensor, new_lens: torch.Tensor,
+                     block_tables: torch.Tensor, context_lens: torch.Tensor,
+                     q_start_loc: Optional[torch.Tensor], positions: Optional[torch.Tensor],
+                     slot_mapping: torch.Tensor, dev_status: Optional[torch.Tensor] = None,
+                     stream=None, bound: bool = False) -> Optional[BoundCall]:
+    """One step's tables from the requests' lengths; see include/pkv.h.  The row buffers
+    (positions, slot_mapping) are filled to their end, padding rows with -1."""
+    index = pool.index
+    B, T = cached_lens.shape[0], slot_mapping.shape[0]
+    rows, one = (T,), (B,)
+    bt_shape = block_tables.shape
+    if not (_is_int32(cached_lens, one, index) and _is_int32(new_lens, one, index)
+            and _is_int32(context_lens, one, index) and _is_int32(slot_mapping, rows, index)
+            and bt_shape[0] == B and _is_int32(block_tables, bt_shape, index)
+            and len(bt_shape) == 2
+            and (q_start_loc is None or _is_int32(q_start_loc, (B + 1,), index))
+            and (positions is None or _is_int32(positions, rows, index))
+            and (dev_status is None or _is_int32(dev_status, dev_status.shape, index))):
+        raise ValueError("pkv_batch_tables: contiguous int32 tensors on the pool's device are wanted: "
+                         "cached_lens, new_lens and context_lens [B], block_tables [B, blocks], "
+                         "q_start_loc [B + 1], positions and slot_mapping [rows]")
+    return _issue(load().pkv_batch_tables,
+                  (pool._ref, cached_lens.data_ptr(), new_lens.data_ptr(), B,
+                   block_tables.data_ptr(), bt_shape[1], context_lens.data_ptr(),
+                   None if q_start_loc is None else q_start_loc.data_ptr(),
+                   None if positions is None else positions.data_ptr(), slot_mapping.data_ptr(), T,
+                   None if dev_status is None else dev_status.data_ptr(),
+                   _stream_on(stream, index)),
+                  "pkv_batch_tables", bound, index)
+
+
+class RopeParams:
+    """The turn that pkv_rope makes: layout "half" or "interleaved", scaling "none",
+    "linear", "base" or "bands" (see include/pkv.h); its frequencies are computed here,
+    once.  ``transposed`` turns by the opposite angle, which is the gradient."""
+
+    def __init__(self, head_dim: int, rotary_dim: Optional[int] = None, layout: str = "half",
+                 theta: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                 low: float = 1.0, high: float = 32.0, original_len: int = 1,
+                 attention_factor: float = 1.0, transposed: bool = False):
+        self.head_dim = int(head_dim)
+        self.rotary_dim = self.head_dim if rotary_dim is None else int(rotary_dim)
+        p = pkv_rope_params(self.rotary_dim, ROPE_LAYOUT[layout], int(transposed),
+                            ROPE_SCALING[scaling], float(theta), float(factor), float(low),
+                            float(high), int(original_len), float(attention_factor))
+        if self.rotary_dim > self.head_dim:
+            raise PkvError(2, "pkv_rope_plan_init")
+        self._plan = pkv_rope_plan()
+        _check(load().pkv_rope_plan_init(ctypes.byref(p), ctypes.byref(self._plan)),
+               "pkv_rope_plan_init")
+        self._ref = ctypes.byref(self._plan)
+
+
+def _rope_rows(name: str, x: torch.Tensor, shape: tuple, dtype, index: int) -> int:
+    """Checks rows [T, heads, D] whose heads lie side by side; their token stride."""
+    st = x.stride()
+    if x.shape != shape or x.dtype is not dtype or x.get_device() != index:
+        raise ValueError(f"{name}: {dtype} {shape} on device {index} is wanted, got {x.dtype} "
+                         f"{tuple(x.shape)} on {x.device}")
+    T, H, D = shape
+    if (st[2] != 1 and D > 1) or (st[1] != D and H > 1):
+        raise ValueError(f"{name}: the heads of a token must lie side by side (strides {st})")
+    return st[0] if T > 1 else 0
+
+
+def pkv_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
+             params: RopeParams, q_out: Optional[torch.Tensor] = None,
+             k_out: Optional[torch.Tensor] = None, stream=None,
+             bound: bool = False) -> Optional[BoundCall]:
+    """Turns the rows of q [T, Hq, D] and k [T, Hkv, D] (k may be None) at their positions,
+    into q_out and k_out or, where those are None, in place; see include/pkv.h.  The rows may
+    be views with any token stride."""
+    shape = q.shape
+    T, Hq, D = shape
+    if D != params.head_dim:
+        raise ValueError(f"q has heads of {D} columns, the parameters {params.head_dim}")
+    index, dtype = q.get_device(), q.dtype
+    if not _is_int32(positions, (T,), index):
+        raise ValueError("positions: a contiguous int32 tensor with one entry for each row of q "
+                         "on q's device is wanted")
+    qp = qop = q.data_ptr()
+    qs = qos = _rope_rows("q", q, shape, dtype, index)
+    if q_out is not None:
+        qop, qos = q_out.data_ptr(), _rope_rows("q_out", q_out, shape, dtype, index)
+    kp = kop = None
+    ks = kos = Hk = 0
+    if k is not None:
+        Hk = k.shape[1]
+        shape = (T, Hk, D)
+        kp = kop = k.data_ptr()
+        ks = kos = _rope_rows("k", k, shape, dtype, index)
+        if k_out is not None:
+            kop, kos = k_out.data_ptr(), _rope_rows("k_out", k_out, shape, dtype, index)
+    return _issue(load().pkv_rope,
+                  (params._ref, qp, qop, qs, qos, Hq, kp, kop, ks, kos, Hk, _CODE[dtype], T, D,
+                   positions.data_ptr(), _stream_on(stream, index)),
+                  "pkv_rope", bound, index)
 
 
 def workspace_for(nbytes: int, device="cuda") -> Optional[torch.Tensor]:
