@@ -35,6 +35,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kPer = 4;                       // requests per thread of a chunk
 constexpr int kChunk = kThreads * kPer;       // requests per chunk
 constexpr int kRowsPerBlock = 1024;
+constexpr int kBackRounds = 8;  // returned pages per thread and round
 constexpr int kMaxBlocks = 1024;  // more rows than 1024 per block are taken in strides
 
 struct TablesArgs {
@@ -51,11 +52,14 @@ struct TablesArgs {
   int B, MB, N, T;
 };
 
+// Prefix sums: new rows, new pages, and pages that ended requests return.
 struct Sums {
-  long long rows, pages;
+  long long rows, need, back;
 };
 
-__device__ __forceinline__ Sums add(Sums a, Sums b) { return {a.rows + b.rows, a.pages + b.pages}; }
+__device__ __forceinline__ Sums add(Sums a, Sums b) {
+  return {a.rows + b.rows, a.need + b.need, a.back + b.back};
+}
 
 // Exclusive block-wide prefix sum; *total receives the block's sum.  The caller
 // synchronises before `part` is used again.
@@ -64,12 +68,13 @@ __device__ __forceinline__ Sums block_scan(Sums v, Sums* part, Sums* total) {
   Sums inc = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const Sums up{__shfl_up_sync(0xffffffffu, inc.rows, o), __shfl_up_sync(0xffffffffu, inc.pages, o)};
+    const Sums up{__shfl_up_sync(0xffffffffu, inc.rows, o), __shfl_up_sync(0xffffffffu, inc.need, o),
+                  __shfl_up_sync(0xffffffffu, inc.back, o)};
     if (lane >= o) inc = add(inc, up);
   }
   if (lane == 31) part[w] = inc;
   __syncthreads();
-  Sums base{0, 0}, all{0, 0};
+  Sums base{0, 0, 0}, all{0, 0, 0};
 #pragma unroll
   for (int i = 0; i < kWarps; ++i) {
     const Sums p = part[i];
@@ -77,31 +82,40 @@ __device__ __forceinline__ Sums block_scan(Sums v, Sums* part, Sums* total) {
     all = add(all, p);
   }
   *total = all;
-  return {base.rows + inc.rows - v.rows, base.pages + inc.pages - v.pages};
+  return {base.rows + inc.rows - v.rows, base.need + inc.need - v.need, base.back + inc.back - v.back};
 }
 
 __device__ __forceinline__ long long pages_of(long long tokens) { return (tokens + kPage - 1) / kPage; }
+
+// The first of n entries of ascending `end` that lies above x (there is one).
+__device__ __forceinline__ int find_above(const int* end, int n, int x) {
+  int l = 0, r = n - 1;
+  while (l < r) {
+    const int m = (l + r) >> 1;
+    if (end[m] > x) r = m;
+    else l = m + 1;
+  }
+  return l;
+}
 
 __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs a) {
   __shared__ int s_end[kChunk];     // end row of each request of the chunk (at most T)
   __shared__ int s_start[kChunk];   // its first row
   __shared__ int s_cached[kChunk];  // its cached tokens, -1 when its rows get no slot
   __shared__ int s_ring[kChunk];    // ring offset of its first new page from the head
+  __shared__ int s_back[kChunk];    // end of its returned pages among the chunk's
   __shared__ Sums s_part[kWarps];
-  __shared__ int s_last, s_any, s_alloc;
-  __shared__ int s_cnt[kWarps];
+  __shared__ int s_last, s_alloc;
+  __shared__ int s_cnt[kBackRounds * kWarps];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int head0 = a.state[0], free0 = a.state[1];
   const bool pool_ok = head0 >= 0 && head0 < a.N && free0 >= 0 && free0 <= a.N;
   const int head = pool_ok ? head0 : 0, count = pool_ok ? free0 : 0;
-  if (tid == 0) {
-    s_any = 0;
-    s_alloc = 0;
-  }
+  const long long cap = static_cast<long long>(a.MB) * kPage;
+  if (tid == 0) s_alloc = 0;
   int bits = pool_ok || blockIdx.x ? 0 : 0x1;  // PKV_DEV_BAD_PAGE
-  __syncthreads();
 
-  long long rows0 = 0, pages0 = 0;  // sums over the chunks before
+  Sums before{0, 0, 0};  // sums over the chunks before
   for (int c0 = 0; c0 < a.B; c0 += kChunk) {
     const bool mine = (c0 / kChunk) % gridDim.x == blockIdx.x;  // this block writes the chunk's outputs
     int c[kPer], n[kPer];
@@ -111,54 +125,61 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs a) {
       c[i] = b < a.B ? a.cached[b] : 0;
       n[i] = b < a.B ? a.fresh[b] : 0;
     }
-    // rows first: a request whose rows pass the end of the row buffers gets no pages
-    long long row_sum = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) row_sum += n[i] > 0 ? n[i] : 0;
-    Sums total;
-    // (pages depend on the rows' prefix only through that end check, so most launches
-    // could scan both at once; the rows that do not fit are found with one extra scan)
-    const Sums at = block_scan({row_sum, 0}, s_part, &total);
-    __syncthreads();
-    long long start = rows0 + at.rows;
-    long long need[kPer], page_sum = 0;
-    bool bad[kPer];
-    int any = 0;
+    Sums sum{0, 0, 0};
+    long long need[kPer], back[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int b = c0 + tid * kPer + i;
-      const long long rows = n[i] > 0 ? n[i] : 0, end = start + rows;
-      bad[i] = c[i] < 0 || c[i] + rows > static_cast<long long>(a.MB) * kPage || (n[i] >= 0 && end > a.T);
-      need[i] = bad[i] || n[i] < 0 ? 0 : pages_of(c[i] + rows) - pages_of(c[i]);
-      page_sum += need[i];
-      if (b < a.B && n[i] < 0 && !bad[i] && c[i] > 0) any = 1;
-      if (mine && b < a.B && bad[i]) bits |= 0x2;  // PKV_DEV_BAD_LEN
-      s_start[tid * kPer + i] = static_cast<int>(start < a.T ? start : a.T);
-      s_end[tid * kPer + i] = static_cast<int>(end < a.T ? end : a.T);
-      start = end;
+      const long long rows = n[i] > 0 ? n[i] : 0;
+      const bool bad = c[i] < 0 || c[i] + rows > cap;
+      need[i] = bad || n[i] < 0 ? 0 : pages_of(c[i] + rows) - pages_of(c[i]);
+      back[i] = bad || n[i] >= 0 ? 0 : pages_of(c[i]);
+      sum = add(sum, {rows, need[i], back[i]});
     }
-    if (any) s_any = 1;
-    Sums page_total;
-    const Sums pg = block_scan({0, page_sum}, s_part, &page_total);
-    long long cum = pages0 + pg.pages;
+    Sums total;
+    Sums at = block_scan(sum, s_part, &total);
+    __syncthreads();
+    if (before.rows + total.rows > a.T) {
+      // some requests' rows pass the end of the row buffers: they get no pages
+      long long end = before.rows + at.rows;
+      sum = {0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        end += n[i] > 0 ? n[i] : 0;
+        if (end > a.T) need[i] = 0;
+        sum.need += need[i];
+      }
+      Sums fitting;
+      at.need = block_scan(sum, s_part, &fitting).need;
+      total.need = fitting.need;
+      __syncthreads();
+    }
+    long long start = before.rows + at.rows, cum = before.need + at.need, gone = at.back;
     int alloc = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int b = c0 + tid * kPer + i, k = tid * kPer + i;
-      const long long before = cum;
+      const long long rows = n[i] > 0 ? n[i] : 0, end = start + rows, first = cum;
+      const bool bad = c[i] < 0 || c[i] + rows > cap || (n[i] >= 0 && end > a.T);
       cum += need[i];
-      const bool live = b < a.B && !bad[i] && n[i] >= 0;
+      gone += back[i];
+      const bool live = b < a.B && !bad && n[i] >= 0;
       const bool served = live && (need[i] == 0 || cum <= count);
       if (served && need[i] > 0) alloc = static_cast<int>(cum);
+      s_start[k] = static_cast<int>(start < a.T ? start : a.T);
+      s_end[k] = static_cast<int>(end < a.T ? end : a.T);
       s_cached[k] = served ? c[i] : -1;
-      s_ring[k] = served ? static_cast<int>(before < count ? before : count) : 0;
+      s_ring[k] = served ? static_cast<int>(first < count ? first : count) : 0;
+      s_back[k] = static_cast<int>(gone < 0x7fffffff ? gone : 0x7fffffff);
       if (mine && b < a.B) {
         a.context[b] = served ? c[i] + n[i] : 0;
         if (a.starts) a.starts[b + 1] = s_end[k];
+        if (bad) bits |= 0x2;             // PKV_DEV_BAD_LEN
         if (live && !served) bits |= 0x20;  // PKV_DEV_NO_PAGES
       }
+      start = end;
     }
     if (alloc) atomicMax(&s_alloc, alloc);
+    before = add(before, total);
     __syncthreads();
     // this block's rows of the chunk
     const int in_chunk = min(kChunk, a.B - c0);
@@ -166,51 +187,47 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs a) {
     for (long long t0 = static_cast<long long>(blockIdx.x) * kRowsPerBlock; t0 < hi;
          t0 += static_cast<long long>(gridDim.x) * kRowsPerBlock) {
       if (t0 + kRowsPerBlock <= lo) continue;
+      // the rows' pages are fetched together, before any table entry is written
+      constexpr int R = kRowsPerBlock / kThreads;
+      int page[R], p[R];
+      int32_t* entry[R];
 #pragma unroll
-      for (int u = 0; u < kRowsPerBlock / kThreads; ++u) {
-        const long long tl = t0 + u * kThreads + tid;
-        if (tl < lo || tl >= hi) continue;
-        const int t = static_cast<int>(tl);
-        int l = 0, r = in_chunk - 1;  // the first request that ends behind row t
-        while (l < r) {
-          const int m = (l + r) >> 1;
-          if (s_end[m] > t) r = m;
-          else l = m + 1;
-        }
+      for (int u = 0; u < R; ++u) {
+        const long long t = t0 + u * kThreads + tid;
+        page[u] = p[u] = -1;
+        entry[u] = nullptr;
+        if (t < lo || t >= hi) continue;
+        const int l = find_above(s_end, in_chunk, static_cast<int>(t));
         const int cached = s_cached[l];
-        int slot = -1, pos = -1;
-        if (cached >= 0) {
-          const int p = cached + (t - s_start[l]);
-          const int pn = p / kPage, have = (cached + kPage - 1) / kPage;
-          int32_t* const entry = a.bt + static_cast<size_t>(c0 + l) * a.MB + pn;
-          int page;
-          if (pn >= have) {
-            const long long q = static_cast<long long>(head) + s_ring[l] + (pn - have);
-            page = a.ring[q >= a.N ? q - a.N : q];
-            if (page < 0 || page >= a.N) page = -1;
-            if (p % kPage == 0) *entry = page;
-          } else {
-            page = *entry;
-          }
-          if (page >= 0 && page < a.N) {
-            slot = page * kPage + p % kPage;
-            pos = p;
-          } else {
-            bits |= 0x1;  // PKV_DEV_BAD_PAGE
-          }
+        if (cached < 0) continue;
+        p[u] = cached + (static_cast<int>(t) - s_start[l]);
+        const int pn = p[u] / kPage, have = (cached + kPage - 1) / kPage;
+        int32_t* const e = a.bt + static_cast<size_t>(c0 + l) * a.MB + pn;
+        if (pn >= have) {
+          const long long q = static_cast<long long>(head) + s_ring[l] + (pn - have);
+          page[u] = a.ring[q >= a.N ? q - a.N : q];
+          if (p[u] % kPage == 0) entry[u] = e;
+        } else {
+          page[u] = *e;
         }
-        a.slots[t] = slot;
-        if (a.positions) a.positions[t] = pos;
+      }
+#pragma unroll
+      for (int u = 0; u < R; ++u) {
+        const long long t = t0 + u * kThreads + tid;
+        if (t < lo || t >= hi) continue;
+        const bool good = page[u] >= 0 && page[u] < a.N;
+        if (entry[u]) *entry[u] = good ? page[u] : -1;
+        if (p[u] >= 0 && !good) bits |= 0x1;  // PKV_DEV_BAD_PAGE
+        a.slots[t] = p[u] >= 0 && good ? page[u] * kPage + p[u] % kPage : -1;
+        if (a.positions) a.positions[t] = good ? p[u] : -1;
       }
     }
-    rows0 += total.rows;
-    pages0 += page_total.pages;
-    __syncthreads();  // the chunk's arrays are free
+    if (c0 + kChunk < a.B) __syncthreads();  // the chunk's arrays are free
   }
   // rows behind the last request: padding
   for (long long t = static_cast<long long>(blockIdx.x) * kThreads + tid; t < a.T;
        t += static_cast<long long>(gridDim.x) * kThreads) {
-    if (t >= rows0) {
+    if (t >= before.rows) {
       a.slots[t] = -1;
       if (a.positions) a.positions[t] = -1;
     }
@@ -229,66 +246,77 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs a) {
       return;
     }
     __threadfence();
+  } else {
+    __syncthreads();
   }
   const int alloc = s_alloc;
   const int room = a.N - (count - alloc);  // places for returned pages
-  long long tail = static_cast<long long>(head) + count;
+  const long long tail = static_cast<long long>(head) + count;
   int pushed = 0;
-  if (s_any && pool_ok) {
+  if (before.back > 0 && pool_ok) {
     for (int c0 = 0; c0 < a.B; c0 += kChunk) {
-      // page offsets of the chunk's ended requests, then all their table entries in order
-      long long mine = 0;
-      long long held[kPer];
+      if (a.B > kChunk) {  // (a single chunk's offsets are still in place)
+        __syncthreads();
+        long long back[kPer], sum = 0;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int b = c0 + tid * kPer + i;
-        const int c = b < a.B ? a.cached[b] : 0;
-        const bool back = b < a.B && a.fresh[b] < 0 && c > 0 && c <= static_cast<long long>(a.MB) * kPage;
-        held[i] = back ? pages_of(c) : 0;
-        mine += held[i];
-      }
-      Sums total;
-      long long at = block_scan({0, mine}, s_part, &total).pages;
-      // (a pool holds at most 2^31 / 16 pages; more table entries than that are cut off)
-      const int n = static_cast<int>(total.pages < 0x7fffffff ? total.pages : 0x7fffffff);
+        for (int i = 0; i < kPer; ++i) {
+          const int b = c0 + tid * kPer + i;
+          const int c = b < a.B ? a.cached[b] : 0;
+          back[i] = b < a.B && a.fresh[b] < 0 && c > 0 && c <= cap ? pages_of(c) : 0;
+          sum += back[i];
+        }
+        Sums total;
+        long long gone = block_scan({0, 0, sum}, s_part, &total).back;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        s_start[tid * kPer + i] = static_cast<int>(at < n ? at : n);
-        at += held[i];
-        s_end[tid * kPer + i] = static_cast<int>(at < n ? at : n);
+        for (int i = 0; i < kPer; ++i) {
+          gone += back[i];
+          s_back[tid * kPer + i] = static_cast<int>(gone < 0x7fffffff ? gone : 0x7fffffff);
+        }
+        __syncthreads();
       }
-      __syncthreads();
-      for (int j0 = 0; j0 < n; j0 += kThreads) {
-        const int j = j0 + tid;
-        int page = -1;
-        if (j < n) {
-          int l = 0, r = kChunk - 1;
-          while (l < r) {
-            const int m = (l + r) >> 1;
-            if (s_end[m] > j) r = m;
-            else l = m + 1;
+      const int n = s_back[kChunk - 1];
+      // table entries in request and page order, kBackRounds of them a thread at a time;
+      // valid ones are numbered by counting them warp by warp
+      for (long long j0 = 0; j0 < n; j0 += kBackRounds * kThreads) {
+        int page[kBackRounds];
+#pragma unroll
+        for (int u = 0; u < kBackRounds; ++u) {
+          const long long j = j0 + u * kThreads + tid;
+          page[u] = -1;
+          if (j < n) {
+            const int l = find_above(s_back, kChunk, static_cast<int>(j));
+            const int first = l ? s_back[l - 1] : 0;
+            page[u] = a.bt[static_cast<size_t>(c0 + l) * a.MB + (j - first)];
           }
-          page = a.bt[static_cast<size_t>(c0 + l) * a.MB + (j - s_start[l])];
-          if (page >= a.N) bits |= 0x1;
         }
-        const bool valid = page >= 0 && page < a.N;
-        const unsigned votes = __ballot_sync(0xffffffffu, valid);
-        if (lane == 0) s_cnt[w] = __popc(votes);
-        __syncthreads();
-        int before = pushed + __popc(votes & ((1u << lane) - 1u)), all = 0;
+        unsigned votes[kBackRounds];
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-          if (i < w) before += s_cnt[i];
-          all += s_cnt[i];
+        for (int u = 0; u < kBackRounds; ++u) {
+          if (page[u] >= a.N) {
+            bits |= 0x1;
+            page[u] = -1;
+          }
+          votes[u] = __ballot_sync(0xffffffffu, page[u] >= 0);
+          if (lane == 0) s_cnt[u * kWarps + w] = __popc(votes[u]);
         }
-        if (valid) {
-          if (before < room) a.ring[(tail + before) % a.N] = page;
-          else bits |= 0x1;  // more pages than the pool has: returned twice
+        __syncthreads();
+        int all = pushed;
+#pragma unroll
+        for (int u = 0; u < kBackRounds; ++u) {
+          int mine = 0;
+#pragma unroll
+          for (int i = 0; i < kWarps; ++i) {
+            if (i == w) mine = all + __popc(votes[u] & ((1u << lane) - 1u));
+            all += s_cnt[u * kWarps + i];
+          }
+          if (page[u] >= 0) {
+            if (mine < room) a.ring[(tail + mine) % a.N] = page[u];
+            else bits |= 0x1;  // more pages than the pool has: returned twice
+          }
         }
-        pushed += all;
+        pushed = all;
         __syncthreads();
       }
-      __syncthreads();
     }
     pushed = pushed < room ? pushed : room;
   }
