@@ -159,6 +159,18 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
       : "memory");
 }
 
+// One-dimensional bulk copy shared -> global (both 16-byte aligned, bytes a multiple of 16),
+// committed as a group of the issuing thread, and the wait for all of that thread's groups
+// (their writes made, their shared memory free again).
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store_wait() {
+  asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 // Four 8x8 b16 matrices from shared memory (lanes 8i..8i+7 give matrix i's row
 // addresses); lane t receives row t/4, elements 2(t%4), 2(t%4)+1 of each matrix.
 __device__ __forceinline__ void ldsm_x2(uint32_t (&f)[2], uint32_t addr) {

@@ -16,10 +16,13 @@
 // that frequency (rounding f itself costs pos * 2^-54 turns); read as a signed number and
 // converted to float it is the angle over pi in [-1, 1], which sincospif takes.
 //
-// One thread owns one token's VE pairs (two 16-byte vectors of every head; VE = 8 for
-// BF16, 4 for float) and walks over the heads: its VE cosines and sines stay in registers,
-// no shared memory, no barrier, and the loads of several heads are in flight at once.  Heads
-// are divided among several threads only while the launch would otherwise not fill the GPU.
+// A block takes a few consecutive tokens.  Their rows come into shared memory by bulk copies
+// (one for a token's query heads, one for its key heads: contiguous kilobytes), while the
+// threads work out each token's cosines and sines once; then every thread turns vector pairs
+// in place (two 16-byte vectors; VE = 8 pairs for BF16, 4 for float) and the rows go out as
+// they came.  So the launch's bytes in flight do not hang on registers or on how many heads a
+// thread walks over, and partly turned heads cost nothing extra.  Rows, strides or sizes
+// that are not multiples of 16 bytes take a plain element-by-element kernel.
 // Bound by HBM: every element is read once and written once.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -31,11 +34,15 @@
 #include "internal.h"
 #include "nvtx.h"
 #include "pkv.h"
+#include "ptx.cuh"
 
 namespace pkv {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kTileBytes = 16 * 1024;   // rows of a block, about
+constexpr int kMaxRowBytes = 96 * 1024;  // of one token, for the bulk-copy kernel
+constexpr int kMaxTile = 32;
 
 struct RopeArgs {
   const void* q;
@@ -45,104 +52,107 @@ struct RopeArgs {
   const int32_t* pos;
   long long qs, ks, qos, kos;  // elements from one token to the next
   int Hq, Hk, T, D, rd;
-  int units;  // threads per token and head group: turned pair vectors, then copied ones
-  int turned;
-  int groups;
+  int tile;    // tokens per block
   float gain, sgn;
   uint64_t freq[PKV_ROPE_MAX_PAIRS];  // turns per position, as a fraction of 2^64
 };
 
-// N consecutive elements as floats
+// Cosine and sine (with the gain) of pair i at a position >= 0.
+__device__ __forceinline__ float2 turn_of(const RopeArgs& a, int pos, int i) {
+  const uint64_t turns = static_cast<uint64_t>(static_cast<uint32_t>(pos)) * a.freq[i];
+  // (scaled by 2^-63: the angle over pi, in [-1, 1])
+  const float x = __ll2float_rn(static_cast<long long>(turns)) * 1.0842021724855044e-19f;
+  float c, s;
+  sincospif(x, &s, &c);
+  return make_float2(c * a.gain, s * a.sgn);
+}
+
+// 16 bytes of elements as they are stored, and as floats.
 template <typename T, int N>
-__device__ __forceinline__ void load(const T* p, float (&x)[N]) {
+__device__ __forceinline__ void widen(uint4 r, float (&x)[N]) {
   if constexpr (sizeof(T) == 2) {
-    if constexpr (N == 8) {
-      const uint4 v = *reinterpret_cast<const uint4*>(p);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
-    } else {
-      x[0] = __bfloat162float(*p);
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   } else {
-    if constexpr (N == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(p);
-      x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
-    } else {
-      x[0] = *p;
-    }
+    x[0] = __uint_as_float(r.x); x[1] = __uint_as_float(r.y);
+    x[2] = __uint_as_float(r.z); x[3] = __uint_as_float(r.w);
   }
 }
 template <typename T, int N>
-__device__ __forceinline__ void store(T* p, const float (&x)[N]) {
+__device__ __forceinline__ uint4 narrow(const float (&x)[N]) {
   if constexpr (sizeof(T) == 2) {
-    if constexpr (N == 8) {
-      uint32_t w[4];
+    uint32_t w[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&v);
-      }
-      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      *p = __float2bfloat16_rn(x[0]);
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&v);
     }
+    return make_uint4(w[0], w[1], w[2], w[3]);
   } else {
-    if constexpr (N == 4) *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    else *p = x[0];
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
   }
 }
 
-// T: element type; VE: pairs per thread (16-byte vectors, or 1 for sizes and strides that
-// are not multiples of them); HALF: half layout, else interleaved.
+// Shared memory: the rows [tile][Hq + Hk][D], the angles [tile][VE / 2][units][2] (two pairs
+// to 16 bytes, so that neighbouring units read neighbouring 16 bytes), the barrier.
 template <typename T, int VE, bool HALF>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
-  const long long idx = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
-  const long long t = idx / a.units;
-  const int j = static_cast<int>(idx - t * a.units);
-  if (t >= a.T) return;
-  const int pos = a.pos[t];
-  if (pos < 0) return;  // padding: the row is left alone
-  const T* q = static_cast<const T*>(a.q) + t * a.qs;
-  const T* k = static_cast<const T*>(a.k) + t * a.ks;
-  T* qo = static_cast<T*>(a.q_out) + t * a.qos;
-  T* ko = static_cast<T*>(a.k_out) + t * a.kos;
-  const int H = a.Hq + a.Hk, D = a.D;
-  auto from = [&](int h) { return h < a.Hq ? q + static_cast<size_t>(h) * D : k + static_cast<size_t>(h - a.Hq) * D; };
-  auto to = [&](int h) { return h < a.Hq ? qo + static_cast<size_t>(h) * D : ko + static_cast<size_t>(h - a.Hq) * D; };
-  if (j >= a.turned) {  // columns that are not turned, copied when the output is elsewhere
-    const int col = a.rd + (j - a.turned) * VE;
-    for (int h = blockIdx.y; h < H; h += a.groups) {
-      if (from(h) == to(h)) continue;
-      float x[VE];
-      load<T, VE>(from(h) + col, x);
-      store<T, VE>(to(h) + col, x);
+__global__ void __launch_bounds__(kThreads) rope_rows_kernel(const __grid_constant__ RopeArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int t0 = blockIdx.x * a.tile, nt = min(a.tile, a.T - t0);
+  const int H = a.Hq + a.Hk, D = a.D, half = a.rd / 2, units = half / VE;
+  const uint32_t qb = a.Hq * D * sizeof(T), kb = a.Hk * D * sizeof(T), row = qb + kb;
+  float* const angles = reinterpret_cast<float*>(smem + static_cast<size_t>(a.tile) * row);
+  uint64_t* const bar = reinterpret_cast<uint64_t*>(angles + 2 * a.tile * half);
+  const int tid = threadIdx.x;
+
+  // warp 0: one lane per token requests (and later returns) its rows; a token at a negative
+  // position is padding and is left alone
+  const bool live = tid < nt && a.pos[t0 + tid] >= 0;
+  if (tid < 32) {
+    const unsigned n = __popc(__ballot_sync(0xffffffffu, live));
+    if (tid == 0) {
+      mbar_init(bar, 1);
+      fence_barrier_init();
+      fence_proxy_async_smem();
+      mbar_arrive_expect_tx(bar, n * row);
     }
+    __syncwarp();
+    if (live) {
+      const uint64_t pol = l2_evict_first_policy();
+      uint8_t* const dst = smem + tid * row;
+      if (qb) bulk_g2s(dst, static_cast<const T*>(a.q) + (t0 + tid) * a.qs, qb, bar, pol);
+      if (kb) bulk_g2s(dst + qb, static_cast<const T*>(a.k) + (t0 + tid) * a.ks, kb, bar, pol);
+    }
+  }
+  for (int i = tid; i < nt * half; i += kThreads) {
+    const int t = i / half, e = i - t * half;
+    const int at = ((e % VE) / 2 * units + e / VE) * 2 + (e & 1);
+    reinterpret_cast<float2*>(angles)[t * half + at] = turn_of(a, max(a.pos[t0 + t], 0), e);
+  }
+  __syncthreads();  // (the barrier is initialised, too)
+  if (!mbar_wait(bar, 0)) {
+    (void)mbar_wait(bar, 0);  // no copy may land in the memory of a block that has left
     return;
   }
-  const int ca = HALF ? j * VE : 2 * j * VE;         // first vector's column
-  const int cb = HALF ? ca + a.rd / 2 : ca + VE;     // second vector's
-  float c[VE], s[VE];
+  const int per_token = H * units;
+  for (int i = tid; i < nt * per_token; i += kThreads) {
+    const int t = i / per_token, r = i - t * per_token, h = r / units, j = r - h * units;
+    uint8_t* const px = smem + t * row + (h * D + (HALF ? j * VE : 2 * j * VE)) * sizeof(T);
+    uint8_t* const py = px + (HALF ? half : VE) * sizeof(T);
+    float c[VE], s[VE];
 #pragma unroll
-  for (int e = 0; e < VE; ++e) {
-    const uint64_t turns = static_cast<uint64_t>(static_cast<uint32_t>(pos)) * a.freq[j * VE + e];
-    // (scaled by 2^-63: the angle over pi, in [-1, 1])
-    const float x = __ll2float_rn(static_cast<long long>(turns)) * 1.0842021724855044e-19f;
-    sincospif(x, &s[e], &c[e]);
-    c[e] *= a.gain;
-    s[e] *= a.sgn;
-  }
-#pragma unroll 4
-  for (int h = blockIdx.y; h < H; h += a.groups) {
-    const T* p = from(h);
-    T* o = to(h);
+    for (int e = 0; e < VE; e += 2) {
+      const float4 v = *reinterpret_cast<const float4*>(angles + 2 * (t * half + (e / 2 * units + j) * 2));
+      c[e] = v.x; s[e] = v.y; c[e + 1] = v.z; s[e + 1] = v.w;
+    }
     float x[VE], y[VE], u[VE], v[VE];
-    load<T, VE>(p + ca, x);
-    load<T, VE>(p + cb, y);
-    if constexpr (HALF || VE == 1) {
+    widen<T, VE>(*reinterpret_cast<const uint4*>(px), x);
+    widen<T, VE>(*reinterpret_cast<const uint4*>(py), y);
+    if constexpr (HALF) {
 #pragma unroll
       for (int e = 0; e < VE; ++e) {
         u[e] = fmaf(x[e], c[e], -(y[e] * s[e]));
@@ -157,15 +167,55 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         v[2 * e + 1] = fmaf(y[2 * e + 1], c[VE / 2 + e], y[2 * e] * s[VE / 2 + e]);
       }
     }
-    store<T, VE>(o + ca, u);
-    store<T, VE>(o + cb, v);
+    *reinterpret_cast<uint4*>(px) = narrow<T, VE>(u);
+    *reinterpret_cast<uint4*>(py) = narrow<T, VE>(v);
+  }
+  fence_proxy_async_smem();  // the turned rows are visible to the copies
+  __syncthreads();
+  if (live) {
+    const uint8_t* const src = smem + tid * row;
+    if (qb) bulk_s2g(static_cast<T*>(a.q_out) + (t0 + tid) * a.qos, src, qb);
+    if (kb) bulk_s2g(static_cast<T*>(a.k_out) + (t0 + tid) * a.kos, src + qb, kb);
+    bulk_store_wait();
   }
 }
 
-template <typename T, int VE>
-const void* kernel_of(bool half) {
-  return half ? reinterpret_cast<const void*>(&rope_kernel<T, VE, true>)
-              : reinterpret_cast<const void*>(&rope_kernel<T, VE, false>);
+// Element by element: one thread per (token, pair or copied column), over the heads.
+template <typename T, bool HALF>
+__global__ void __launch_bounds__(kThreads) rope_elements_kernel(const __grid_constant__ RopeArgs a) {
+  const int half = a.rd / 2, units = half + a.D - a.rd;
+  const long long idx = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
+  const long long t = idx / units;
+  const int j = static_cast<int>(idx - t * units);
+  if (t >= a.T) return;
+  const int pos = a.pos[t];
+  if (pos < 0) return;
+  const bool turned = j < half;
+  const int ca = !turned ? a.rd + j - half : HALF ? j : 2 * j, cb = HALF ? ca + half : ca + 1;
+  const float2 cs = turned ? turn_of(a, pos, j) : make_float2(0.f, 0.f);
+  for (int h = 0; h < a.Hq + a.Hk; ++h) {
+    const bool isq = h < a.Hq;
+    const size_t at = static_cast<size_t>(isq ? h : h - a.Hq) * a.D;
+    const T* p = isq ? static_cast<const T*>(a.q) + t * a.qs + at : static_cast<const T*>(a.k) + t * a.ks + at;
+    T* o = isq ? static_cast<T*>(a.q_out) + t * a.qos + at : static_cast<T*>(a.k_out) + t * a.kos + at;
+    if (!turned) {
+      if (p != o) o[ca] = p[ca];
+      continue;
+    }
+    const float x = static_cast<float>(p[ca]), y = static_cast<float>(p[cb]);
+    o[ca] = static_cast<T>(fmaf(x, cs.x, -(y * cs.y)));
+    o[cb] = static_cast<T>(fmaf(y, cs.x, x * cs.y));
+  }
+}
+
+template <typename T>
+const void* kernel_of(bool rows, bool half) {
+  constexpr int VE = 16 / sizeof(T);
+  if (rows)
+    return half ? reinterpret_cast<const void*>(&rope_rows_kernel<T, VE, true>)
+                : reinterpret_cast<const void*>(&rope_rows_kernel<T, VE, false>);
+  return half ? reinterpret_cast<const void*>(&rope_elements_kernel<T, true>)
+              : reinterpret_cast<const void*>(&rope_elements_kernel<T, false>);
 }
 
 // Turns per position of pair i as a fraction of 2^64 (frequencies are below one turn).
@@ -256,10 +306,11 @@ extern "C" pkv_status pkv_rope(const pkv_rope_plan* plan, const void* q, void* q
                           (num_kv_heads ? reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(k_out) : 0);
   if (bases % elt || !pkv::aligned4(positions)) return PKV_ERR_ALIGN;
   const long long strides = (num_q_heads ? a.qs | a.qos : 0) | (num_kv_heads ? a.ks | a.kos : 0);
-  // 16-byte vectors when every row, every head and both halves of the turned columns start
-  // on a 16-byte boundary; single elements otherwise
-  const bool vec = bases % 16 == 0 && strides % ve == 0 && head_dim % ve == 0 && (rd / 2) % ve == 0;
-  const int per = vec ? ve : 1;
+  // bulk copies and 16-byte vectors when every row, every head and both halves of the turned
+  // columns start on a 16-byte boundary; single elements otherwise
+  const long long per_token = (qrow + krow) * elt;
+  const bool rows = bases % 16 == 0 && strides % ve == 0 && head_dim % ve == 0 && (rd / 2) % ve == 0 &&
+                    per_token <= pkv::kMaxRowBytes;
   a.q = q;
   a.k = k;
   a.q_out = q_out;
@@ -270,26 +321,33 @@ extern "C" pkv_status pkv_rope(const pkv_rope_plan* plan, const void* q, void* q
   a.T = num_tokens;
   a.D = head_dim;
   a.rd = rd;
-  a.turned = rd / 2 / per;
-  const bool elsewhere = (num_q_heads && q != q_out) || (num_kv_heads && k != k_out);
-  a.units = a.turned + (elsewhere ? (head_dim - rd) / per : 0);
   a.gain = plan->attention_factor;
   a.sgn = plan->transposed ? -a.gain : a.gain;
   for (int i = 0; i < rd / 2; ++i) a.freq[i] = plan->freq[i];
-  // Heads per thread: all of them once the tokens alone give every SM a few hundred threads.
-  const long long threads = static_cast<long long>(num_tokens) * a.units;
-  const int H = num_q_heads + num_kv_heads;
-  const long long want = 152 * 512;
-  long long groups = threads >= want ? 1 : (want + threads - 1) / threads;
-  a.groups = static_cast<int>(groups > H ? H : groups);
-  const long long blocks = (threads + pkv::kThreads - 1) / pkv::kThreads;
+  long long blocks;
+  size_t smem = 0;
+  if (rows) {
+    // Tokens per block: about kTileBytes of rows, fewer while that would leave SMs without a
+    // block (a decode step's tokens get a block each).
+    long long tile = pkv::kTileBytes / per_token;
+    const long long spread = (num_tokens + 152 * 4 - 1) / (152 * 4);
+    if (tile > spread) tile = spread;
+    if (tile > pkv::kMaxTile) tile = pkv::kMaxTile;
+    if (tile < 1) tile = 1;
+    a.tile = static_cast<int>(tile);
+    blocks = (num_tokens + tile - 1) / tile;
+    smem = static_cast<size_t>(tile) * (per_token + (rd / 2) * sizeof(float2)) + 16;
+  } else {
+    blocks = (static_cast<long long>(num_tokens) * (rd / 2 + head_dim - rd) + pkv::kThreads - 1) / pkv::kThreads;
+  }
   if (blocks > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
-  const void* fn;
   const bool half = plan->layout == PKV_ROPE_HALF;
-  if (dtype == PKV_F32) fn = vec ? pkv::kernel_of<float, 4>(half) : pkv::kernel_of<float, 1>(half);
-  else fn = vec ? pkv::kernel_of<__nv_bfloat16, 8>(half) : pkv::kernel_of<__nv_bfloat16, 1>(half);
+  const void* fn = dtype == PKV_F32 ? pkv::kernel_of<float>(rows, half) : pkv::kernel_of<__nv_bfloat16>(rows, half);
+  if (smem > 48 * 1024 &&  // (rows of very many heads)
+      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024) != cudaSuccess)
+    return PKV_ERR_LAUNCH;
   void* args[] = {&a};
-  const cudaError_t e = cudaLaunchKernel(fn, dim3(static_cast<unsigned>(blocks), a.groups), dim3(pkv::kThreads), args,
-                                         0, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = cudaLaunchKernel(fn, dim3(static_cast<unsigned>(blocks)), dim3(pkv::kThreads), args, smem,
+                                         static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PKV_OK : PKV_ERR_LAUNCH;
 }
