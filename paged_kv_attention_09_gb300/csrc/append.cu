@@ -7,6 +7,7 @@
 // the shared quantisers (kvrow.cuh).  INT4 K rows are written as whole 32-bit words and
 // INT4 V bytes belong to one token each, so tokens of one call never share a byte.
 #include <cuda_bf16.h>
+#include <math_constants.h>
 
 #include "internal.h"
 #include "kvrow.cuh"
@@ -117,149 +118,196 @@ __global__ void __launch_bounds__(kWarps * 32)
 
 // Block-scaled 8-bit formats: the scale belongs to the 16 tokens of a (page, kv head), so
 // the new rows of one page are taken together.  They stand next to each other in the call in
-// ascending order of their slots (a run); the run's first token leads: one warp per (leader,
-// kv head, K or V) finds the largest new value, grows the block's scale to hold it (rows
-// before the run's first offset keep their place and are coded again when it grows; a run
-// that starts the page starts its scale afresh), and stores the run.  The other tokens'
-// warps leave at once.
+// ascending order of their slots (a run).  One warp takes the runs that start within `group`
+// consecutive tokens, for one kv head and one of K and V; for each run it finds the largest
+// new value, grows the block's scale to hold it (rows before the run's first offset keep
+// their place and are coded again when it grows; a run that starts the page starts its scale
+// afresh), and stores the run.
 //
 // The old block is fetched whole, 16 bytes a lane, together with the new rows, before the
 // scale is known: a decode step's append then waits for one round trip after the slots'.
 // A V block has its tokens along the rows, so its bytes are merged in registers and stored
 // as whole 16-byte rows; K rows are stored as they are, old rows only when coded again.
+constexpr int kBlockWarps = 4;
+
+// Four values -> the four stored bytes at scale s (inv = 1 / s: exact for FP8B, whose scales
+// are powers of two; rounded for INT8B, NaN where 1 / s is not a normal number).
+template <bool FP8>
+__device__ __forceinline__ uint32_t block_codes4(float a, float b, float c, float d, float s, float inv) {
+  if (s == 0.f) return FP8 ? 0u : 0x80808080u;
+  if constexpr (FP8) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a * inv, b * inv), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c * inv, d * inv), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+  } else {
+    // Adding 1.5 * 2^23 rounds to the nearest whole number, ties to even, and leaves
+    // code + 128 in the low byte.  x * inv is within 2 units in the last place (2^-16 up to
+    // 127) of the quotient, so it rounds to the same code unless it lies that near a half:
+    // then, and for anything not finite, the division itself is taken.
+    constexpr float kMagic = 12583040.f;
+    const float y[4] = {a * inv, b * inv, c * inv, d * inv};
+    float far = 0.f;
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float m = y[i] + kMagic;
+      u[i] = __float_as_uint(m);
+      const float off = fabsf(y[i] - (m - kMagic));
+      asm("max.NaN.f32 %0, %0, %1;" : "+f"(far) : "f"(off));
+    }
+    if (!(far < 0.4999f)) {
+      const float x[4] = {a, b, c, d};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        u[i] = __float_as_uint(fminf(fmaxf(__fdiv_rn(x[i], s), -127.f), 127.f) + kMagic);
+    }
+    return __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+  }
+}
+// Four stored bytes coded again (block_recode), where `keep` has ones.
+template <bool FP8>
+__device__ __forceinline__ uint32_t block_recode4(uint32_t w, float by) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) m |= block_recode<FP8>((w >> (8 * b)) & 0xffu, by) << (8 * b);
+  return m;
+}
+
 template <bool FP8, int NEW_DT, int D>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kBlockWarps * 32)
     append_block_kernel(uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache,
                         float* __restrict__ k_scale, float* __restrict__ v_scale,
                         const void* __restrict__ k_new, const void* __restrict__ v_new,
-                        const int32_t* __restrict__ slots, int T, int Hkv, int num_pages,
+                        const int32_t* __restrict__ slots, int T, int Hkv, int num_pages, int group,
                         int32_t* dev_status) {
   constexpr int E = D / 32;  // head-dim elements per lane; also 16-byte pieces of a block
   const int lane = threadIdx.x & 31;
-  const long long item = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const long long item = static_cast<long long>(blockIdx.x) * kBlockWarps + (threadIdx.x >> 5);
   const int which = static_cast<int>(item & 1);
-  const long long th = item >> 1;
-  if (th >= static_cast<long long>(T) * Hkv) return;
-  const int tok = static_cast<int>(th / Hkv), h = static_cast<int>(th % Hkv);
-  // slots of this token, the one before (lane 16) and the 15 after it (lanes 1 .. 15)
-  const int idx = lane < 16 ? tok + lane : tok - 1;
-  const int s_at = lane <= 16 && idx >= 0 && idx < T ? slots[idx] : -1;
-  const int slot = __shfl_sync(0xffffffffu, s_at, 0), prev = __shfl_sync(0xffffffffu, s_at, 16);
-  if (slot < 0) return;
-  if (slot >= num_pages * kPage) {
-    if (lane == 0 && dev_status) atomicOr(dev_status, 0x4 /*PKV_DEV_BAD_SLOT*/);
-    return;
-  }
-  const int page = slot / kPage, off = slot % kPage;
-  if (prev >= 0 && prev / kPage == page) {
-    // not a leader; out of order it belongs to no run
-    if (prev + 1 != slot && lane == 0 && dev_status) atomicOr(dev_status, 0x4);
-    return;
-  }
-  // the run: tokens tok .. tok + n - 1 at offsets off .. off + n - 1
-  const unsigned follow = __ballot_sync(0xffffffffu, lane < 16 && lane + off < kPage && s_at == slot + lane);
-  const int n = __ffs(~follow) - 1;
-  const size_t blk = static_cast<size_t>(page) * Hkv + h;
-  uint8_t* const block = (which ? v_cache : k_cache) + blk * kPage * D;
-  float* const scale = (which ? v_scale : k_scale) + blk;
+  const int h = static_cast<int>((item >> 1) % Hkv);
+  const long long base = (item >> 1) / Hkv * group;  // the first of the warp's tokens
+  if (base >= T) return;
+  // slots: lane 0 the token before the group, lanes 1 .. group its own, then those behind
+  const long long at0 = base - 1 + lane;
+  const int slot = at0 >= 0 && at0 < T ? slots[at0] : -1;
+  const int prev = __shfl_up_sync(0xffffffffu, slot, 1);
+  const bool mine = lane >= 1 && lane <= group && slot >= 0;
+  const bool inside = slot < num_pages * kPage;
+  const bool joined = prev >= 0 && prev / kPage == slot / kPage;  // its page's run started before
+  if (mine && (!inside || (joined && prev + 1 != slot)) && h == 0 && which == 0 && dev_status)
+    atomicOr(dev_status, 0x4 /*PKV_DEV_BAD_SLOT*/);
+  unsigned leaders = __ballot_sync(0xffffffffu, mine && inside && !joined);
   const void* const src = which ? v_new : k_new;
 
-  // old block (only where bytes of it may stay: rows before the run; V also rows behind it):
-  // K 16-byte pieces lane + 32 i, V the 16 token bytes of head-dim rows lane * E + i
-  const bool old_rows = off > 0, fetch = which ? n < kPage : old_rows;
-  float s_old = old_rows ? *scale : 0.f;
-  uint4 was[E];
+  while (leaders) {
+    const int lead = __ffs(leaders) - 1;
+    leaders &= leaders - 1;
+    // the run: tokens tok .. tok + n - 1 at offsets off .. off + n - 1 of the page
+    const int first = __shfl_sync(0xffffffffu, slot, lead);
+    const long long tok = base - 1 + lead;
+    const int page = first / kPage, off = first % kPage;
+    const unsigned follow = __ballot_sync(0xffffffffu, lane >= lead && slot == first + (lane - lead) &&
+                                                           off + (lane - lead) < kPage);
+    const int n = __ffs(~(follow >> lead)) - 1;
+    const size_t blk = static_cast<size_t>(page) * Hkv + h;
+    uint8_t* const block = (which ? v_cache : k_cache) + blk * kPage * D;
+    float* const scale = (which ? v_scale : k_scale) + blk;
+
+    // old block (only where bytes of it may stay: rows before the run; V also rows behind
+    // it): K 16-byte pieces lane + 32 i, V the 16 token bytes of head-dim rows lane * E + i
+    const bool old_rows = off > 0, fetch = which ? n < kPage : old_rows;
+    const float s_old = old_rows ? *scale : 0.f;
+    uint4 was[E];
 #pragma unroll
-  for (int i = 0; i < E; ++i)
-    was[i] = fetch ? reinterpret_cast<const uint4*>(block)[which ? lane * E + i : lane + 32 * i]
-                   : make_uint4(0u, 0u, 0u, 0u);
-  float x[kPage][E];  // the token at page offset t, elements lane * E ..
-  float amax = 0.f;
+    for (int i = 0; i < E; ++i)
+      was[i] = fetch ? reinterpret_cast<const uint4*>(block)[which ? lane * E + i : lane + 32 * i]
+                     : make_uint4(0u, 0u, 0u, 0u);
+    float x[kPage][E];  // the token at page offset t, elements lane * E ..
+    float amax = 0.f;
 #pragma unroll
-  for (int t = 0; t < kPage; ++t) {
+    for (int t = 0; t < kPage; ++t) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[t][e] = 0.f;
-    if (t >= off && t < off + n) {
-      const size_t at = (static_cast<size_t>(tok + t - off) * Hkv + h) * D + lane * E;
-      if constexpr (NEW_DT == kBF16) {
-        const uint32_t* p = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(src) + at);
+      for (int e = 0; e < E; ++e) x[t][e] = 0.f;
+      if (t >= off && t < off + n) {
+        const size_t at = (static_cast<size_t>(tok + t - off) * Hkv + h) * D + lane * E;
+        if constexpr (NEW_DT == kBF16) {
+          uint32_t v[E / 2];
+          if constexpr (E == 4) {
+            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(src) + at);
+            v[0] = u.x;
+            v[E / 2 - 1] = u.y;
+          } else {
+            v[0] = *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(src) + at);
+          }
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const uint32_t v = p[e / 2];
-          x[t][e] = __uint_as_float(v << 16);
-          x[t][e + 1] = __uint_as_float(v & 0xffff0000u);
-        }
-      } else {
-        const float2* p = reinterpret_cast<const float2*>(static_cast<const float*>(src) + at);
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float2 v = p[e / 2];
-          x[t][e] = v.x;
-          x[t][e + 1] = v.y;
+          for (int e = 0; e < E; e += 2) {
+            x[t][e] = __uint_as_float(v[e / 2] << 16);
+            x[t][e + 1] = __uint_as_float(v[e / 2] & 0xffff0000u);
+          }
+        } else if constexpr (E == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(src) + at);
+          x[t][0] = v.x; x[t][1] = v.y; x[t][2] = v.z; x[t][3] = v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(static_cast<const float*>(src) + at);
+          x[t][0] = v.x; x[t][1] = v.y;
         }
       }
     }
-  }
 #pragma unroll
-  for (int t = 0; t < kPage; ++t)
+    for (int t = 0; t < kPage; ++t)
 #pragma unroll
-    for (int e = 0; e < E; ++e) amax = fmaxf(amax, fabsf(x[t][e]));
+      for (int e = 0; e < E; ++e) amax = fmaxf(amax, fabsf(x[t][e]));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const float need = block_scale<FP8>(amax);
-  const float s = old_rows ? fmaxf(s_old, need) : need;
-  const bool again = old_rows && s > s_old;
-  const float by = again ? __fdiv_rn(s_old, s) : 1.f;
-  if (lane == 0) *scale = s;
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const float need = block_scale<FP8>(amax);
+    const float s = old_rows ? fmaxf(s_old, need) : need;
+    const bool again = old_rows && s > s_old;
+    const float by = again ? __fdiv_rn(s_old, s) : 1.f;
+    float inv = s != 0.f ? __fdiv_rn(1.f, s) : 0.f;
+    if (!FP8 && !(s > 1e-37f && s < 1e37f)) inv = CUDART_NAN_F;  // (takes the division)
+    if (lane == 0) *scale = s;
 
-  if (which == 0) {  // K: a row of D bytes per token
-    if (again) {
+    if (which == 0) {  // K: a row of D bytes per token
+      if (again) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+          if ((lane + 32 * i) * 16 / D >= off) continue;
+          reinterpret_cast<uint4*>(block)[lane + 32 * i] =
+              make_uint4(block_recode4<FP8>(was[i].x, by), block_recode4<FP8>(was[i].y, by),
+                         block_recode4<FP8>(was[i].z, by), block_recode4<FP8>(was[i].w, by));
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < kPage; ++t) {
+        if (t < off || t >= off + n) continue;
+        uint8_t* const row = block + t * D + lane * E;
+        const uint32_t m = block_codes4<FP8>(x[t][0], x[t][1], x[t][E - 2], x[t][E - 1], s, inv);
+        if constexpr (E == 4) *reinterpret_cast<uint32_t*>(row) = m;
+        else *reinterpret_cast<uint16_t*>(row) = static_cast<uint16_t>(m);
+      }
+    } else {  // V: 16 token bytes per head-dim row; the lane's rows are lane * E ..
+      // byte masks of the run's tokens and of the rows before it
+      uint32_t m_new[4], m_old[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int lo = min(max(off - 4 * u, 0), 4), hi = min(max(off + n - 4 * u, 0), 4);
+        const uint32_t below = lo == 4 ? ~0u : (1u << (8 * lo)) - 1u;
+        m_old[u] = below;
+        m_new[u] = (hi == 4 ? ~0u : (1u << (8 * hi)) - 1u) & ~below;
+      }
 #pragma unroll
       for (int i = 0; i < E; ++i) {
-        if ((lane + 32 * i) * 16 / D >= off) continue;
         uint32_t w[4] = {was[i].x, was[i].y, was[i].z, was[i].w};
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          uint32_t m = 0;
-#pragma unroll
-          for (int b = 0; b < 4; ++b) m |= block_recode<FP8>((w[u] >> (8 * b)) & 0xffu, by) << (8 * b);
-          w[u] = m;
+          if (again && m_old[u]) w[u] = (w[u] & ~m_old[u]) | (block_recode4<FP8>(w[u], by) & m_old[u]);
+          if (m_new[u])
+            w[u] = (w[u] & ~m_new[u]) |
+                   (block_codes4<FP8>(x[4 * u][i], x[4 * u + 1][i], x[4 * u + 2][i], x[4 * u + 3][i], s, inv) &
+                    m_new[u]);
         }
-        reinterpret_cast<uint4*>(block)[lane + 32 * i] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4*>(block)[lane * E + i] = make_uint4(w[0], w[1], w[2], w[3]);
       }
-    }
-#pragma unroll
-    for (int t = 0; t < kPage; ++t) {
-      if (t < off || t >= off + n) continue;
-      uint32_t m = 0;
-#pragma unroll
-      for (int e = 0; e < E; ++e) m |= block_code<FP8>(x[t][e], s) << (8 * e);
-      uint8_t* const row = block + t * D + lane * E;
-      if constexpr (E == 4) *reinterpret_cast<uint32_t*>(row) = m;
-      else *reinterpret_cast<uint16_t*>(row) = static_cast<uint16_t>(m);
-    }
-  } else {  // V: 16 token bytes per head-dim row; the lane's rows are lane * E ..
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const uint32_t w[4] = {was[i].x, was[i].y, was[i].z, was[i].w};
-      uint32_t out[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int t = 4 * u + b;
-          uint32_t byte = (w[u] >> (8 * b)) & 0xffu;
-          if (t < off) {
-            if (again) byte = block_recode<FP8>(byte, by);
-          } else if (t < off + n) {
-            byte = block_code<FP8>(x[t][i], s);
-          }
-          m |= byte << (8 * b);
-        }
-        out[u] = m;
-      }
-      reinterpret_cast<uint4*>(block)[lane * E + i] = make_uint4(out[0], out[1], out[2], out[3]);
     }
   }
 }
@@ -268,14 +316,18 @@ template <bool FP8>
 cudaError_t launch_block(const CacheView& c, void* k, void* v, float* ks, float* vs, const void* kn,
                          const void* vn, int new_dtype, const int32_t* slots, int T,
                          int32_t* dev_status, cudaStream_t st) {
-  const long long items = 2ll * T * c.Hkv;
-  const dim3 grid(static_cast<unsigned>((items + kWarps - 1) / kWarps));
+  // Tokens per warp: one while every token can have its own warps at once (a decode step's
+  // tokens each lie in a page of their own), else 8 (a prompt's tokens share pages: with
+  // one token per warp, 15 of 16 warps only find that they do not lead a run).
+  const int group = 2ll * T * c.Hkv <= 152 * 16 ? 1 : 8;
+  const long long items = 2ll * ((T + group - 1) / group) * c.Hkv;
+  const dim3 grid(static_cast<unsigned>((items + kBlockWarps - 1) / kBlockWarps));
   uint8_t* kb = static_cast<uint8_t*>(k);
   uint8_t* vb = static_cast<uint8_t*>(v);
   const bool nb = new_dtype == kBF16;
 #define PKV_BLOCK(ND, DD)                                                                      \
-  append_block_kernel<FP8, ND, DD><<<grid, kWarps * 32, 0, st>>>(kb, vb, ks, vs, kn, vn, slots, \
-                                                                 T, c.Hkv, c.num_pages, dev_status)
+  append_block_kernel<FP8, ND, DD><<<grid, kBlockWarps * 32, 0, st>>>(                         \
+      kb, vb, ks, vs, kn, vn, slots, T, c.Hkv, c.num_pages, group, dev_status)
   if (c.D == 64) {
     if (nb) PKV_BLOCK(kBF16, 64);
     else PKV_BLOCK(kF32, 64);
