@@ -34,7 +34,6 @@ int sm_count(int device) {
 
 bool plan_prefill(const CacheView& c, int B, int Hq, int max_q_len, int MB, int q_dtype,
                   int device, const PrefillOpts& opts, PrefillPlan* plan) {
-  (void)MB;
   if (c.dtype != kBF16 && !block_scaled(c.dtype)) return false;
   if (c.D != 64 && c.D != 128) return false;
   const int G = Hq / c.Hkv;
@@ -53,7 +52,10 @@ bool plan_prefill(const CacheView& c, int B, int Hq, int max_q_len, int MB, int 
   if (opts.key_split > 0) {
     best = opts.key_split;
   } else {
-    while (best < 3 && tiles > 0 && tiles * (best + 1) <= slots) ++best;
+    // (block-scaled caches: at least 512 keys of the table's width per block, below which the
+    // merge costs more than it saves: 37 tokens over 41 take 12.8 us split in 3 and 9.5 us unsplit)
+    const int most = !block_scaled(c.dtype) ? 3 : static_cast<int>(static_cast<long long>(MB) * kPage / 512);
+    while (best < 3 && best < most && tiles > 0 && tiles * (best + 1) <= slots) ++best;
   }
   if (tiles * best > 0x7fffffffLL / 2) best = 1;
   plan->ksplit = best;

@@ -8,27 +8,39 @@
 // scores, s_v its 16 probabilities.
 //
 // One block computes 128 query rows, (chunk token, query head) pairs of one GQA group,
-// token-major, against the group's keys in pairs of 64-key tiles (8 pages):
-//   warps 9-12   K: fetch the pair's codes 16 bytes a thread, one pair ahead in registers,
-//                and write them as FP16 operand tiles (no-swizzle K-major core matrices);
-//                they also leave the pages' scales in a ring of four pairs;
-//   warps 13-16  V: the same per 64-key tile; codes of keys that no row sees become zero
-//                (a stale E4M3 NaN would survive a zero probability);
-//   warp 8       one thread issues every MMA: S(p) = Q K^T (M = 128, N = 128) into one of
-//                two score buffers of TMEM, O_g += P_g V (M = 128, N = head_dim) for the
-//                two softmax groups g;
-//   warps 0-7    softmax, two groups of four warps, one thread per row; group g takes the
-//                pair's tile g with its own running max and sum and its own accumulator
-//                O_g, merged once at the end.  P overwrites its own scores in TMEM, page by
-//                page (8 columns of FP16 high parts, 8 of remainders: P keeps ~22 bits, two
-//                MMAs per page), so that two score buffers fit beside the accumulators: the
-//                scores of pair p + 1 are ready while the groups work on pair p.
+// token-major, against the group's keys in tiles of 128 (8 pages):
+//   warps 18-20  K: each takes every third run of 64 keys (4 pages).  Its codes come by bulk
+//                copies into a slot of the warp's own, requested as soon as the slot is free
+//                (a warp fetches for itself: no hand-over), and are written as FP16 operand
+//                blocks (no-swizzle K-major core matrices); the pages' scales are copied into
+//                a ring of eight tiles;
+//   warps 21-23  V: the same; codes of keys that no row sees become zero (a stale E4M3 NaN
+//                would survive a zero probability).  (Two warps for float queries, whose
+//                second operand tile takes the room.)  A shared-memory round trip takes some
+//                150 cycles in this kernel, so a page's loads are in flight together and every
+//                wait, fence and arrival stands for 64 keys: one page a time and warp, each with
+//                its own, took 2700 cycles a page;
+//   warp 16      one thread issues S(i) = Q K^T (M = 128, N = 128) into one of three score
+//                buffers of TMEM, warp 17 one thread O += P(i) V (M = 128, N = head_dim):
+//                two issuers, since each barrier that one asks costs it as much as two MMAs;
+//   warps 0-15   softmax, four threads per row, 32 keys each.  They share the row's running
+//                maximum: it is raised only when a score passes it by 2^8, so nearly every
+//                tile costs the four warps of 32 rows one barrier with a vote, not an exchange.  P overwrites
+//                its own scores in TMEM, page by page (8 columns of FP16 high parts, 8 of
+//                remainders: P keeps ~22 bits, two MMAs per page), so that three score
+//                buffers fit beside the accumulator.
+// What bounds it: a tile takes ~2400 cycles, of which the softmax's exponentials take 1024 on
+// the special-function pipe; they do not overlap with the same warps' loads, votes and waits
+// (~1300), since the four warps of a scheduler are the four parts of the same rows.  The MMAs
+// take 1600 and the fills less.  Measured (cycles a tile; 4 x 512 tokens over 4096, 12 / 2 heads
+// of 128, FP8B): 4400 with the codes through registers or asynchronous copies and one MMA
+// issuer, 3300 with whole runs of 64 keys per warp and no bank conflicts, 2600 with two issuers.
+// That workload: 52.0 us, 655 TFLOP/s; 2 chunks of 512 over 2048: 33.6 us.
 //
 // Range of FP16: query rows are brought to [2^13, 2^14) by a power of two that goes into the
 // score scale (float queries as high part + remainder); probabilities carry the V scale as
 // 2^(log2 s_v + lg), lg raised or lowered when a page's scale leaves the range, so that
-// P s_v stays below 2^15.  The sum takes P s_v / s_v, so the rounding of the logarithm
-// cancels.
+// P s_v stays below 2^15; the sum takes P s_v / 2^(log2 s_v + lg) back off.
 // Every wait is bounded.
 #include <cuda_fp16.h>
 #include <math_constants.h>
@@ -43,19 +55,23 @@
 namespace pkv {
 namespace {
 
-constexpr int kSoftWarps = 8;  // two groups of 4 warps, one thread per query row
+constexpr int kParts = 4;                // softmax threads per query row
+constexpr int kSoftWarps = 4 * kParts;
 constexpr int kSoftThreads = kSoftWarps * 32;
 constexpr int kMmaWarp = kSoftWarps;
-constexpr int kKWarp = kMmaWarp + 1;
-constexpr int kFillWarps = 4;  // warps that fill each of the K and V rings
-constexpr int kVWarp = kKWarp + kFillWarps;
-constexpr int kThreadsB = (kVWarp + kFillWarps) * 32;
-constexpr int kPairPages = 2 * kPagesTC;
-constexpr int kScaleSlots = 4;
-constexpr float kGainTop = 7.f;  // log2 of the largest scaled V scale
+constexpr int kPvWarp = kMmaWarp + 1;
+constexpr int kKWarp = kPvWarp + 1;
+constexpr int kKWarps = 3;                // warps that fill the K ring
+constexpr int kVWarp = kKWarp + kKWarps;
+constexpr int kKeysB = 128;               // keys per tile
+constexpr int kPagesB = kKeysB / kPage;
+constexpr int kPartKeys = kKeysB / kParts, kPartPages = kPagesB / kParts;
+constexpr int kScores = 3;               // score buffers
+constexpr int kScaleSlots = 8;
+constexpr float kGainTop = 7.f;          // log2 of the largest scaled V scale
 
 #ifdef PKV_TEST_HOOKS
-// Test builds only: each softmax group's first wait for scores gives up at once.
+// Test builds only: the softmax threads' first wait for scores gives up at once.
 __device__ int g_test_prefill_blk_fail_first_wait = 0;
 #endif
 
@@ -63,30 +79,52 @@ template <int D, bool QSPLIT>
 struct BSmem {
   static constexpr int blk = kPage * D * 2;          // one FP16 page block (K or V)
   static constexpr int qTile = kRowsTC * D * 2;      // one FP16 query tile
-  static constexpr int KSP = 2;                      // stages of the K ring (a tile pair each)
-  static constexpr int KST = 4;                      // stages of the V ring (a tile each)
-  static constexpr int kStage = kPairPages * blk, vStage = kPagesTC * blk;
+  static constexpr int half = kPagesTC * blk;        // operand blocks of 64 keys
+  static constexpr int KST = 2;                      // K ring: tiles
+  static constexpr int VST = QSPLIT ? 3 : 4;         // V ring: halves
+  static constexpr int VW = QSPLIT ? 2 : 3;          // warps that fill the V ring
+  static constexpr int threads = (kVWarp + VW) * 32;
+  static constexpr int page = kPage * D;             // a page's codes
+  static constexpr int raw = kPagesTC * page;        // a warp's slot: the codes of 64 keys
   static constexpr int q0 = 0;
   static constexpr int k0 = q0 + (QSPLIT ? 2 : 1) * qTile;
-  static constexpr int v0 = k0 + KSP * kStage;
-  // scales of a pair's pages: K scale [8], log2 of the V scale [8], 1 / V scale [8]
-  static constexpr int sc0 = v0 + KST * vStage;
-  static constexpr int scSlot = 3 * kPairPages * 4;
+  static constexpr int v0 = k0 + KST * 2 * half;
+  static constexpr int rk0 = v0 + VST * half;
+  static constexpr int rv0 = rk0 + kKWarps * raw;
+  // scales of a tile's pages: K [8], V [8]
+  static constexpr int sc0 = rv0 + VW * raw;
+  static constexpr int scSlot = 2 * kPagesB * 4;
   static constexpr int bar0 = sc0 + kScaleSlots * scSlot;
   // barriers by index
-  static constexpr int kFull = 0, kEmpty = 2, vFull = 4, vEmpty = 8, sFull = 12, pFull = 14, oDone = 18,
-                       fin = 20, xfin = 21, qFull = 22, nbars = 24;
-  static constexpr int misc0 = bar0 + nbars * 8;  // TMEM base address, abort flag
-  // row maxima of the queries, then the final exchange (max, sum, gain by group and row),
-  // then the split merge's weights
-  static constexpr int xch0 = misc0 + 16;
-  static constexpr int total = xch0 + 4 * kRowsTC * 4 + 2 * kRowsTC * 4;
-  // TMEM columns: O of group 0 [0, D), O of group 1 [D, 2D), score buffers at 2D + 128 b
-  // (group g's 64 keys at + 64 g)
-  static constexpr int sCol = 2 * D;
+  static constexpr int kFull = 0, kEmpty = 2, vFull = 4, vEmpty = 8, sFull = 12, pFull = 15, oDone = 17,
+                       fin = 19, qFull = 20, rawFull = 21, nbars = rawFull + kKWarps + VW;
+  static constexpr int misc0 = bar0 + (nbars + nbars % 2) * 8;  // TMEM base address, abort flag; failed waits of the softmax quarters
+  // row values exchanged by the softmax threads [part][row]; then the split merge's weights
+  static constexpr int xch0 = misc0 + 32;
+  static constexpr int total = xch0 + kParts * kRowsTC * 4;
+  // TMEM columns: O [0, D), score buffer i at 128 + 128 i (part h's 32 keys at + 32 h)
+  static constexpr int sCol = 128;
   static constexpr int tmemCols = 512;
-  static_assert(2 * D + 4 * kKeysTC <= 512, "tensor memory");
+  static_assert(sCol + kScores * kKeysB <= 512 && D <= sCol, "tensor memory");
+  static_assert(total <= 227 * 1024, "shared memory");
 };
+
+// The four softmax warps of one TMEM lane quarter hold the four parts of the same 32 rows;
+// quarters are independent of each other.  A vote of a quarter's threads (and their barrier),
+// and their barrier alone.
+__device__ __forceinline__ bool quarter_any(int quarter, bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(p)), "r"(1 + quarter), "n"(32 * kParts)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void quarter_sync(int quarter) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(5 + quarter), "n"(32 * kParts) : "memory");
+}
 
 // Four stored bytes -> their four code values in FP16, in order.
 template <bool FP8>
@@ -103,35 +141,54 @@ __device__ __forceinline__ void codes4(uint32_t w, uint32_t& lo, uint32_t& hi) {
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
   }
 }
-// 16 stored bytes -> two 16-byte operand rows of 8 FP16 values, `step` bytes apart.
+// 4 bytes global -> shared asynchronously, and the groups they complete in.
+__device__ __forceinline__ void fetch4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>  // all but the N latest groups have landed
+__device__ __forceinline__ void fetch_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// 16 stored bytes -> two 16-byte operand rows of 8 FP16 values, 128 bytes apart.
 template <bool FP8>
-__device__ __forceinline__ void store_codes16(uint8_t* dst, uint32_t step, uint4 c) {
+__device__ __forceinline__ void store_codes16(uint8_t* dst, uint4 c) {
   uint4 a, b;
   codes4<FP8>(c.x, a.x, a.y);
   codes4<FP8>(c.y, a.z, a.w);
   codes4<FP8>(c.z, b.x, b.y);
   codes4<FP8>(c.w, b.z, b.w);
   *reinterpret_cast<uint4*>(dst) = a;
-  *reinterpret_cast<uint4*>(dst + step) = b;
+  *reinterpret_cast<uint4*>(dst + 128) = b;
+}
+
+__device__ __forceinline__ float fast_log2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // (a, b) -> f16x2 high part and f16x2 remainder
 __device__ __forceinline__ void split2(float2 a, uint32_t& hi, uint32_t& lo) {
   const __half2 h = __float22half2_rn(a);
-  const float2 f = __half22float2(h);
-  const __half2 r = __float22half2_rn(__fadd2_rn(a, make_float2(-f.x, -f.y)));
   hi = *reinterpret_cast<const uint32_t*>(&h);
+  float x, y;  // a - h, each one multiply-add of the FP16 part by -1
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "fma.rn.f32.f16 %0, l, %5, %3;\n\tfma.rn.f32.f16 %1, h, %5, %4;\n\t}"
+      : "=f"(x), "=f"(y)
+      : "r"(hi), "f"(a.x), "f"(a.y), "h"(static_cast<unsigned short>(0xBC00)));
+  const __half2 r = __floats2half2_rn(x, y);
   lo = *reinterpret_cast<const uint32_t*>(&r);
 }
 
 template <bool FP8, int D, bool QSPLIT>
-__global__ void __launch_bounds__(kThreadsB, 1)
+__global__ void __launch_bounds__(BSmem<D, QSPLIT>::threads, 1)
     prefill_blk_kernel(const __grid_constant__ TParams p) {
   using Sm = BSmem<D, QSPLIT>;
-  extern __shared__ __align__(1024) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Sm::bar0);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Sm::misc0);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Sm::misc0 + 4);
+  volatile int* soft_fail = reinterpret_cast<volatile int*>(smem + Sm::misc0 + 16);
   __shared__ int s_err;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -159,12 +216,12 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   const int lo_max = win > 0 ? p_last - win + 1 : 0;
   const int kb0 = (lo_blk / kPage) * kPage;
   // this block's share of the key tiles: [t0, t1) of the row tile's range
-  const int nt_all = err ? 0 : (n_keys0 - kb0 + kKeysTC - 1) / kKeysTC;
+  const int nt_all = err ? 0 : (n_keys0 - kb0 + kKeysB - 1) / kKeysB;
   const int t0 = ks * nt_all / p.ksplit, t1 = (ks + 1) * nt_all / p.ksplit;
-  const int n_keys = err ? 0 : min(n_keys0, kb0 + t1 * kKeysTC);
-  const int kbase = err ? 0 : kb0 + t0 * kKeysTC;
+  const int n_keys = err ? 0 : min(n_keys0, kb0 + t1 * kKeysB);
+  const int kbase = err ? 0 : kb0 + t0 * kKeysB;
   const int n_pages = max(0, (n_keys - kbase + kPage - 1) / kPage);  // pages from kbase on
-  const int n_tiles = t1 - t0, n_pairs = (n_tiles + 1) / 2;
+  const int n_tiles = t1 - t0;
   const int32_t* btw = p.bt + static_cast<size_t>(b) * p.MB + kbase / kPage;
 
   // ---- set-up: TMEM and barriers
@@ -174,15 +231,15 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   }
   if (tid == 0) {
     for (int i = 0; i < Sm::nbars; ++i) {
-      const bool filled = (i >= Sm::kFull && i < Sm::kFull + 2) || (i >= Sm::vFull && i < Sm::vFull + 4);
-      const int count = filled                                       ? kFillWarps
-                        : i >= Sm::pFull && i < Sm::pFull + 4        ? kSoftThreads / 2
-                        : i == Sm::xfin || i == Sm::qFull            ? kSoftThreads
-                                                                     : 1;
+      const int count = i >= Sm::kFull && i < Sm::kFull + Sm::KST     ? 2   // its halves
+                        : i == Sm::pFull || i == Sm::pFull + 1 || i == Sm::qFull ? kSoftWarps
+                        : i == Sm::fin                                ? 2  // one from each MMA issuer
+                                                                      : 1;
       mbar_init(&bars[i], count);
     }
     fence_barrier_init();
     *abort_flag = 0;
+    for (int i = 0; i < 4; ++i) soft_fail[i] = 0;
     s_err = err;
   }
   tc::fence_before_sync();
@@ -191,11 +248,12 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   const uint32_t tmem = *tmem_slot;
   const uint32_t sbase = smem_u32(smem);
 
-  // softmax threads: row r (= TMEM lane 32 (warp % 4) + lane) of group grp
+  // softmax threads: row r (= TMEM lane 32 (warp % 4) + lane), part of the row
   const int r = tid & (kRowsTC - 1);
-  const int grp = tid / kRowsTC;
+  const int part = tid / kRowsTC;
   const int rho = row0 + r;
   const bool valid_row = tid < kSoftThreads && rho < nrows;
+  const int quarter = warp & 3;
 
   // A page id outside the pool is replaced by page 0 (every read stays inside the cache)
   // and flagged: the block's rows then become NaN.
@@ -208,177 +266,173 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     return 0;
   };
 
-  if (n_tiles > 0 && warp >= kKWarp && warp < kVWarp) {
-    // ---------------------------------------------------------------- K codes
-    // thread -> 16 codes of one token; the 8 lanes of a quarter warp take 8 tokens, so that
-    // their 16-byte operand rows are one core matrix (no bank conflicts)
-    constexpr int PPS = D == 128 ? 1 : 2;             // pages per step of the four warps
-    constexpr int STEPS = kPairPages / PPS;
-    const int w = warp - kKWarp;
-    const int sub = D == 128 ? 0 : w >> 1;
-    const int row = 8 * (D == 128 ? w >> 1 : w & 1) + (lane & 7);
-    const int piece = (D == 128 ? 4 * (w & 1) : 0) + (lane >> 3);
-    const uint8_t* src = p.k + static_cast<size_t>(g) * kPage * D + row * D + piece * 16;
-    const size_t stride = static_cast<size_t>(p.Hkv) * kPage * D;
-    uint8_t* dst = smem + Sm::k0 + tile_off(sub * kPage + row, 16 * piece, D);
-    uint4 raw[STEPS];
-    float sk = 0.f, sv = 0.f;
-    auto fetch1 = [&](int s, int ids) {
-      const int id = __shfl_sync(0xffffffffu, ids, s * PPS + sub);
-      raw[s] = id >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + id * stride)) : make_uint4(0u, 0u, 0u, 0u);
-    };
-    auto fetch_scales = [&](int ids) {
-      sk = sv = 0.f;
-      if (w == 0 && lane < kPairPages && ids >= 0) {
-        sk = p.ks[static_cast<size_t>(ids) * p.Hkv + g];
-        sv = p.vs[static_cast<size_t>(ids) * p.Hkv + g];
+  constexpr int UPP = D / 32;  // units of 32 pieces of 16 codes per page
+  const int n_halves = 2 * n_tiles;
+  if (n_tiles > 0 && warp >= kKWarp) {
+    // ---------------------------------------------------------------- K and V codes
+    const bool isK = warp < kVWarp;
+    const int step = isK ? kKWarps : Sm::VW, w = warp - (isK ? kKWarp : kVWarp);
+    const uint32_t slot = sbase + (isK ? Sm::rk0 : Sm::rv0) + w * Sm::raw;
+    const uint32_t bar = smem_u32(&bars[Sm::rawFull + warp - kKWarp]);
+    const uint64_t pol = l2_evict_last_policy();  // every row tile of the group rereads them
+    const uint8_t* const src = isK ? p.k : p.v;
+    // the ids of the warp's next 64 keys (lanes 0 .. 3), loaded one run ahead: read when
+    // needed they would cost a global round trip
+    int ids = page_id(kPagesTC * w + (lane & 3));
+    auto request = [&](int h) {  // the copies of run h, h = w, w + step, ...
+      if (h < n_halves) {
+        const int n = min(kPagesTC, max(0, n_pages - kPagesTC * h));  // its pages
+        mbar_arrive_expect_tx_if(lane == 0, bar, n * Sm::page);
+        const bool there = lane < n;
+        const size_t blk = there ? static_cast<size_t>(ids) * p.Hkv + g : 0;
+        __syncwarp();
+        bulk_g2s_if(there, slot + lane * Sm::page, src + blk * Sm::page, Sm::page, bar, pol);
+        if (isK && lane < kPagesTC) {
+          const uint32_t at = sbase + Sm::sc0 + (h >> 1) % kScaleSlots * Sm::scSlot + ((h & 1) * kPagesTC + lane) * 4;
+          if (there) {
+            fetch4(at, p.ks + blk);
+            fetch4(at + 4 * kPagesB, p.vs + blk);
+          } else {  // no page: zeros (its keys are masked)
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(0) : "memory");
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 4 * kPagesB), "r"(0) : "memory");
+          }
+        }
+        ids = page_id(kPagesTC * (h + step) + (lane & 3));
       }
+      fetch_commit();
     };
-    int ids = page_id(lane & 7);
-#pragma unroll
-    for (int s = 0; s < STEPS; ++s) fetch1(s, ids);
-    fetch_scales(ids);
-    ids = page_id(kPairPages + (lane & 7));
+    request(w);
     bool ok = true;
-    for (int j = 0; j < n_pairs; ++j) {
-      const int st = j % Sm::KSP;
-      if (j >= Sm::KSP) ok = mbar_wait_warp(smem_u32(&bars[Sm::kEmpty + st]), (j / Sm::KSP - 1) & 1);
-      if (!ok || *abort_flag) break;
-      const bool more = j + 1 < n_pairs;
-      if (w == 0 && lane < kPairPages) {
-        // (an all-zero block has scale 0 and zero codes: any K scale gives its zeros; a V
-        // scale of 0, and pages past the end, are marked by a logarithm of -inf)
-        float* sc = reinterpret_cast<float*>(smem + Sm::sc0 + (j % kScaleSlots) * Sm::scSlot);
-        sc[lane] = sk == 0.f ? 1.f : sk;
-        sc[kPairPages + lane] = sv == 0.f ? -CUDART_INF_F : log2f(sv);
-        sc[2 * kPairPages + lane] = sv == 0.f ? 1.f : 1.f / sv;
-      }
-      if (more) fetch_scales(ids);
+    uint32_t phase = 0;
+    int h = w;
+    // K: thread -> 16 codes of one token, a piece of its D / 16.  The 8 lanes of a quarter warp
+    // take 8 tokens along a diagonal, so that both their loads (rows of D bytes) and their
+    // stores (16-byte rows of core matrices) fall into different banks.  V: the 16 tokens of
+    // one head-dim row, unit u: rows 32 u .. + 31.
+    uint32_t from[UPP], to[UPP];
 #pragma unroll
-      for (int s = 0; s < STEPS; ++s) {
-        store_codes16<FP8>(dst + st * Sm::kStage + s * PPS * Sm::blk, 128, raw[s]);
-        if (more) fetch1(s, ids);
+    for (int u = 0; u < UPP; ++u) {
+      const int l = lane & 7, k = lane >> 3;
+      const int row = l + 8 * (D == 128 ? u >> 1 : u);
+      const int piece = D == 128 ? (l + k + 4 * (u & 1)) & 7 : ((l >> 1) + k) & 3;
+      from[u] = slot + (isK ? row * D + piece * 16 : lane * 16 + 512 * u);
+      to[u] = isK ? tile_off(row, 16 * piece, D) : bf16_v_off(lane, 0) + 1024 * u;
+    }
+    for (; h < n_halves; h += step, phase ^= 1) {
+      const int j = h >> 1, st = isK ? j % Sm::KST : h % Sm::VST, use = isK ? j / Sm::KST : h / Sm::VST;
+      if (use > 0)
+        ok = mbar_wait_warp(smem_u32(&bars[(isK ? Sm::kEmpty : Sm::vEmpty) + st]), (use - 1) & 1);
+      ok = mbar_wait_warp(bar, phase) && ok;
+      if (!ok) break;
+      uint8_t* const dst = smem + (isK ? Sm::k0 + (2 * st + (h & 1)) * Sm::half : Sm::v0 + st * Sm::half);
+      const int key0 = kbase + h * kKeysTC;
+      const int n = min(kPagesTC, max(0, n_pages - kPagesTC * h));
+      const bool edge = !isK && (key0 < lo_blk || key0 + kKeysTC > n_keys);
+      auto load = [&](int q, uint4 (&c)[UPP]) {
+#pragma unroll
+        for (int u = 0; u < UPP; ++u) c[u] = lds_u4(from[u] + q * Sm::page);
+      };
+      uint4 cur[UPP], nxt[UPP];
+      load(0, cur);
+#pragma unroll
+      for (int q = 0; q < kPagesTC; ++q) {
+        if (q + 1 < kPagesTC) load(q + 1, nxt);
+        if (q >= n) {
+#pragma unroll
+          for (int u = 0; u < UPP; ++u) cur[u] = make_uint4(0u, 0u, 0u, 0u);
+        } else if (edge) {  // only tokens that some row sees
+          const int key = key0 + q * kPage;
+          uint32_t m[4];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            m[v] = 0u;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int t = key + 4 * v + e;
+              if (t >= lo_blk && t < n_keys) m[v] |= 0xffu << (8 * e);
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < UPP; ++u) {
+            cur[u].x &= m[0]; cur[u].y &= m[1]; cur[u].z &= m[2]; cur[u].w &= m[3];
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < UPP; ++u) {
+          store_codes16<FP8>(dst + q * Sm::blk + to[u], cur[u]);
+          cur[u] = nxt[u];
+        }
       }
       fence_proxy_async_smem();
+      fetch_wait<0>();  // this run's scales
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[Sm::kFull + st]);
-      ids = page_id((j + 2) * kPairPages + (lane & 7));
+      if (lane == 0) mbar_arrive(&bars[(isK ? Sm::kFull : Sm::vFull) + st]);
+      request(h + step);  // (every lane has read the slot)
     }
     if (!ok) *abort_flag = 1;
+    // leave nothing in flight
+    fetch_wait<0>();
+    if (h < n_halves) (void)mbar_wait_warp(bar, phase);
     if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&s_err, 0x1);  // PKV_DEV_BAD_PAGE
-  } else if (n_tiles > 0 && warp >= kVWarp) {
-    // ---------------------------------------------------------------- V codes
-    // thread -> the 16 tokens of one head-dim row of a page: two operand rows of 8 tokens
-    constexpr int PPS = D == 128 ? 1 : 2;
-    constexpr int STEPS = kPagesTC / PPS;  // per tile
-    const int w = warp - kVWarp;
-    const int sub = D == 128 ? 0 : w >> 1;
-    const int d = (D == 128 ? 32 * w : 32 * (w & 1)) + lane;
-    const uint8_t* src = p.v + static_cast<size_t>(g) * kPage * D + d * 16;
-    const size_t stride = static_cast<size_t>(p.Hkv) * kPage * D;
-    uint8_t* dst = smem + Sm::v0 + sub * Sm::blk + bf16_v_off(d, 0);
-    uint4 raw[2][STEPS];  // the two tiles of a pair
-    auto fetch1 = [&](int y, int s, int ids) {
-      const int id = __shfl_sync(0xffffffffu, ids, y * kPagesTC + s * PPS + sub);
-      raw[y][s] = id >= 0 ? __ldg(reinterpret_cast<const uint4*>(src + id * stride)) : make_uint4(0u, 0u, 0u, 0u);
-    };
-    int ids = page_id(lane & 7);
-#pragma unroll
-    for (int y = 0; y < 2; ++y)
-#pragma unroll
-      for (int s = 0; s < STEPS; ++s) fetch1(y, s, ids);
-    ids = page_id(kPairPages + (lane & 7));
-    bool ok = true;
-    for (int j = 0; j < n_pairs && ok; ++j) {
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int i = 2 * j + y, st = i % Sm::KST;
-        if (i >= n_tiles) break;
-        if (i >= Sm::KST) ok = mbar_wait_warp(smem_u32(&bars[Sm::vEmpty + st]), (i / Sm::KST - 1) & 1);
-        if (*abort_flag) ok = false;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-          uint4 c = raw[y][s];
-          const int key = kbase + i * kKeysTC + (s * PPS + sub) * kPage;  // of the page's token 0
-          if (key < lo_blk || key + kPage > n_keys) {  // only tokens that some row sees
-            uint32_t m[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              m[u] = 0u;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int t = key + 4 * u + e;
-                if (t >= lo_blk && t < n_keys) m[u] |= 0xffu << (8 * e);
-              }
-            }
-            c.x &= m[0]; c.y &= m[1]; c.z &= m[2]; c.w &= m[3];
-          }
-          store_codes16<FP8>(dst + st * Sm::vStage + s * PPS * Sm::blk, 128, c);
-          if (j + 1 < n_pairs) fetch1(y, s, ids);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[Sm::vFull + st]);
-      }
-      ids = page_id((j + 2) * kPairPages + (lane & 7));
-    }
-    if (!ok) *abort_flag = 1;
-    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(&s_err, 0x1);
-  } else if (n_tiles > 0 && warp == kMmaWarp) {
+  } else if (n_tiles > 0 && (warp == kMmaWarp || warp == kPvWarp)) {
     // ---------------------------------------------------------------- MMA issue
     if (lane == 0) {
-      constexpr uint32_t idS = tc::idesc_f16_f32(kRowsTC, 2 * kKeysTC);
+      constexpr uint32_t idS = tc::idesc_f16_f32(kRowsTC, kKeysB);
       constexpr uint32_t idO = tc::idesc_f16_f32(kRowsTC, D);
       constexpr uint32_t sboQK = (D / 8) * 128;  // 8-row groups of Q and of K
       const uint64_t dQhi = tc::smem_desc(sbase + Sm::q0, 128, sboQK);
       const uint64_t dQlo = tc::smem_desc(sbase + Sm::q0 + Sm::qTile, 128, sboQK);
       const uint64_t dK0 = tc::smem_desc(sbase + Sm::k0, 128, sboQK);
       const uint64_t dV0 = tc::smem_desc(sbase + Sm::v0, 128, 256);
-      // S of pair pr, once the last readers of its buffer, the P.V products of pair pr - 2,
-      // have completed (only MMAs into one accumulator are bound to run in order)
-      auto issue_s = [&](int pr) -> bool {
-        if (pr >= 2 && (!mbar_wait(&bars[Sm::oDone], pr & 1) || !mbar_wait(&bars[Sm::oDone + 1], pr & 1)))
-          return false;
-        if (!mbar_wait(&bars[Sm::kFull + pr % Sm::KSP], (pr / Sm::KSP) & 1) || *abort_flag) return false;
-        tc::fence_after_sync();
-        const uint64_t dK = tc::desc_add(dK0, (pr % Sm::KSP) * Sm::kStage);
-        const uint32_t tS = tmem + Sm::sCol + 2 * kKeysTC * (pr & 1);
+      auto done_bar = [&](int i) { return &bars[Sm::oDone + (i & 1)]; };
+      bool ok = true;
+      if (warp == kMmaWarp) {
+        // S of tile i, once its K is there and the last readers of its buffer, the P.V products
+        // of tile i - 3, have completed
+        ok = mbar_wait(&bars[Sm::qFull], 0);
+        for (int i = 0; i < n_tiles && ok; ++i) {
+          ok = (i < kScores || mbar_wait(done_bar(i - kScores), ((i - kScores) >> 1) & 1)) &&
+               mbar_wait(&bars[Sm::kFull + i % Sm::KST], (i / Sm::KST) & 1) && !*abort_flag;
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint64_t dK = tc::desc_add(dK0, (i % Sm::KST) * 2 * Sm::half);
+          const uint32_t tS = tmem + Sm::sCol + kKeysB * (i % kScores);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint64_t bd = tc::desc_add(dK, k * 256);
-          tc::mma_bf16(tS, tc::desc_add(dQhi, k * 256), bd, idS, k > 0);
-          if constexpr (QSPLIT) tc::mma_bf16(tS, tc::desc_add(dQlo, k * 256), bd, idS, true);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t bd = tc::desc_add(dK, k * 256);
+            tc::mma_bf16(tS, tc::desc_add(dQhi, k * 256), bd, idS, k > 0);
+            if constexpr (QSPLIT) tc::mma_bf16(tS, tc::desc_add(dQlo, k * 256), bd, idS, true);
+          }
+          tc::commit(&bars[Sm::sFull + i % kScores]);
+          tc::commit(&bars[Sm::kEmpty + i % Sm::KST]);
         }
-        tc::commit(&bars[Sm::sFull + (pr & 1)]);
-        tc::commit(&bars[Sm::kEmpty + pr % Sm::KSP]);
-        return true;
-      };
-      auto issue_pv = [&](int i) -> bool {
-        const int y = i & 1, pr = i >> 1, st = i % Sm::KST;
-        if (!mbar_wait(&bars[Sm::pFull + 2 * y + (pr & 1)], (pr >> 1) & 1)) return false;
-        if (!mbar_wait(&bars[Sm::vFull + st], (i / Sm::KST) & 1) || *abort_flag) return false;
-        tc::fence_after_sync();
-        const uint64_t dV = tc::desc_add(dV0, st * Sm::vStage);
-        const uint32_t tP = tmem + Sm::sCol + 2 * kKeysTC * (pr & 1) + kKeysTC * y;
+      } else {
+        // O += P V of tile i
+        for (int i = 0; i < n_tiles && ok; ++i) {
+          for (int h = 2 * i; h < 2 * i + 2 && ok; ++h)
+            ok = mbar_wait(&bars[Sm::vFull + h % Sm::VST], (h / Sm::VST) & 1);
+          ok = ok && mbar_wait(&bars[Sm::pFull + (i & 1)], (i >> 1) & 1) && !*abort_flag;
+          if (!ok) break;
+          tc::fence_after_sync();
+          const uint32_t tP = tmem + Sm::sCol + kKeysB * (i % kScores);
 #pragma unroll
-        for (int q = 0; q < kPagesTC; ++q) {
-          const uint64_t bd = tc::desc_add(dV, q * Sm::blk);
+          for (int y = 0; y < 2; ++y) {
+            const int st = (2 * i + y) % Sm::VST;
+            const uint64_t dV = tc::desc_add(dV0, st * Sm::half);
 #pragma unroll
-          for (int part = 0; part < 2; ++part)
-            tc::mma_bf16_ts(tmem + D * y, tP + 16 * q + 8 * part, bd, idO, !(i < 2 && q == 0 && part == 0));
+            for (int q = 0; q < kPagesTC; ++q) {
+              const uint64_t bd = tc::desc_add(dV, q * Sm::blk);
+#pragma unroll
+              for (int half = 0; half < 2; ++half)
+                tc::mma_bf16_ts(tmem, tP + 16 * (kPagesTC * y + q) + 8 * half, bd, idO,
+                                !(i == 0 && y == 0 && q == 0 && half == 0));
+            }
+            tc::commit(&bars[Sm::vEmpty + st]);
+          }
+          // (two barriers in turn: whoever waits for one of tile i's products may come after
+          // those of tile i + 1 have completed)
+          tc::commit(done_bar(i));
         }
-        tc::commit(&bars[Sm::oDone + y]);
-        tc::commit(&bars[Sm::vEmpty + st]);
-        return true;
-      };
-      bool ok = mbar_wait(&bars[Sm::qFull], 0);
-      for (int pr = 0; pr < min(2, n_pairs) && ok; ++pr) ok = issue_s(pr);
-      for (int pr = 0; pr < n_pairs && ok; ++pr) {
-        ok = issue_pv(2 * pr);
-        if (ok && 2 * pr + 1 < n_tiles) ok = issue_pv(2 * pr + 1);
-        if (ok && pr + 2 < n_pairs) ok = issue_s(pr + 2);
       }
       if (!ok) *abort_flag = 1;
       // every MMA has completed before TMEM is released
@@ -387,15 +441,15 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     }
   } else if (n_tiles > 0 && warp < kSoftWarps) {
     // ---------------------------------------------------------------- the query rows
-    // each thread brings half of its row's columns; the two halves exchange their largest
+    // each thread brings its part of its row's columns; the parts exchange their largest
     // value, and the row becomes FP16 in [2^13, 2^14)
-    float* xch = reinterpret_cast<float*>(smem + Sm::xch0);
+    float* xch = reinterpret_cast<float*>(smem + Sm::xch0);  // [part][row]
     float rs;
     {
-      constexpr int N = D / 2;
+      constexpr int N = D / kParts;
       float x[N];
       if (valid_row) {
-        const size_t at = (static_cast<size_t>(q0 + rho / p.G) * p.Hq + g * p.G + rho % p.G) * D + N * grp;
+        const size_t at = (static_cast<size_t>(q0 + rho / p.G) * p.Hq + g * p.G + rho % p.G) * D + N * part;
         if constexpr (!QSPLIT) {
           const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + at);
 #pragma unroll
@@ -423,9 +477,10 @@ __global__ void __launch_bounds__(kThreadsB, 1)
       float top = 0.f;
 #pragma unroll
       for (int i = 0; i < N; ++i) top = fmaxf(top, fabsf(x[i]));
-      xch[grp * kRowsTC + r] = top;
-      asm volatile("bar.sync 1, %0;" ::"n"(kSoftThreads) : "memory");
-      top = fmaxf(top, xch[(grp ^ 1) * kRowsTC + r]);
+      xch[part * kRowsTC + r] = top;
+      quarter_sync(quarter);
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) top = fmaxf(top, xch[i * kRowsTC + r]);
       // top in [2^(e-1), 2^e): times 2^k, k = 14 - e
       const int e = static_cast<int>((__float_as_uint(top) >> 23) & 0xffu) - 126;
       const int k = min(14 - e, 126);
@@ -438,74 +493,85 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 #pragma unroll
         for (int u = 0; u < 4; ++u)
           split2(make_float2(x[8 * c + 2 * u] * f, x[8 * c + 2 * u + 1] * f), h[u], l[u]);
-        const uint32_t off = tile_off(r, N * grp + 8 * c, D);
+        const uint32_t off = tile_off(r, N * part + 8 * c, D);
         *reinterpret_cast<uint4*>(qhi + off) = make_uint4(h[0], h[1], h[2], h[3]);
         if constexpr (QSPLIT) *reinterpret_cast<uint4*>(qhi + Sm::qTile + off) = make_uint4(l[0], l[1], l[2], l[3]);
       }
       fence_proxy_async_smem();
-      mbar_arrive(&bars[Sm::qFull]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[Sm::qFull]);
     }
     // ---------------------------------------------------------------- softmax rows
     const int pos = valid_row ? L - Lq + rho / p.G : p_first;
     const int lo_row = win > 0 ? pos - win + 1 : 0;  // first key of the row's window
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t tO = tmem + lane_base + D * grp;
+    constexpr int DP = D / kParts;  // columns of O that this thread rescales and writes
+    const uint32_t tO = tmem + lane_base + DP * part;
     float m_used = -CUDART_INF_F, l = 0.f;
     float lg = 100.f;  // log2 of the gain on the V scales (the first tile brings it down)
     bool ok = true;
-    int n_mine = 0;  // tiles this group has finished
-    for (int j = grp; j < n_tiles; j += 2, ++n_mine) {
-      const int k = j >> 1;  // the pair
-      ok = mbar_wait(&bars[Sm::sFull + (k & 1)], (k >> 1) & 1) && !*abort_flag;
+    // A quarter's threads pass the same barriers in every tile, whatever happens: a wait that
+    // gave up only raises soft_fail, which all of them see in the same tile.
+    int i = 0;
+    for (; i < n_tiles; ++i) {
+      ok = mbar_wait_warp(smem_u32(&bars[Sm::sFull + i % kScores]), (i / kScores) & 1) && ok;
 #ifdef PKV_TEST_HOOKS
-      if (k == 0 && g_test_prefill_blk_fail_first_wait) ok = false;  // a wait that gives up
+      if (i == 0 && g_test_prefill_blk_fail_first_wait) ok = false;  // a wait that gives up
 #endif
-      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       tc::fence_after_sync();
-      const uint32_t tS = tmem + lane_base + Sm::sCol + 2 * kKeysTC * (k & 1) + kKeysTC * grp;
-      float s[64];
-      tc::ld64(tS, s);
-      const float* sc = reinterpret_cast<const float*>(smem + Sm::sc0 + (k % kScaleSlots) * Sm::scSlot) +
-                        kPagesTC * grp;
-      const float4 k4 = *reinterpret_cast<const float4*>(sc);
-      const float4 v4 = *reinterpret_cast<const float4*>(sc + kPairPages);
-      const float4 i4 = *reinterpret_cast<const float4*>(sc + 2 * kPairPages);
+      const uint32_t tS = tmem + lane_base + Sm::sCol + kKeysB * (i % kScores) + kPartKeys * part;
+      const float* sc = reinterpret_cast<const float*>(smem + Sm::sc0 + (i % kScaleSlots) * Sm::scSlot);
+      const float2 k2 = *reinterpret_cast<const float2*>(sc + kPartPages * part);
+      const float2 v2 = *reinterpret_cast<const float2*>(sc + kPagesB + kPartPages * part);
       // (never 0: a masked score of -inf has to stay -inf; 1e-37 takes every score to 0)
       constexpr float kTiny = 1e-37f;
-      const float kf[4] = {fmaxf(k4.x * rs, kTiny), fmaxf(k4.y * rs, kTiny), fmaxf(k4.z * rs, kTiny),
-                           fmaxf(k4.w * rs, kTiny)};
-      const float lv[4] = {v4.x, v4.y, v4.z, v4.w};
-      const float iv[4] = {i4.x, i4.y, i4.z, i4.w};
-      const int key0 = kbase + j * kKeysTC;
-      if (key0 + kKeysTC - 1 > p_first || key0 + kKeysTC > n_keys || key0 < lo_max) {
+      const float kf[2] = {fmaxf(k2.x * rs, kTiny), fmaxf(k2.y * rs, kTiny)};
+      const float lv[2] = {fast_log2(v2.x), fast_log2(v2.y)};  // (-inf: a page of zeros, or none)
+      const float4 va = *reinterpret_cast<const float4*>(sc + kPagesB), vb = *reinterpret_cast<const float4*>(sc + kPagesB + 4);
+      const float lv_top = fast_log2(fmaxf(fmax3(fmax3(va.x, va.y, va.z), fmax3(va.w, vb.x, vb.y), vb.z), vb.w));
+      float s[kPartKeys];
+      __syncwarp();
+      tc::ld32(tS, s);
+      const int key0 = kbase + i * kKeysB + kPartKeys * part;
+      if (key0 + kPartKeys - 1 > p_first || key0 + kPartKeys > n_keys || key0 < lo_max) {
 #pragma unroll
-        for (int u = 0; u < 64; ++u)
+        for (int u = 0; u < kPartKeys; ++u)
           s[u] = (key0 + u <= pos && key0 + u >= lo_row) ? s[u] : -CUDART_INF_F;
       }
       // largest score: raw per page (the scales are positive), then scaled
       float mx = -CUDART_INF_F;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float t[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) t[u] = fmaxf(s[16 * q + u], s[16 * q + 8 + u]);
-        mx = fmaxf(mx, kf[q] * fmax3(fmax3(t[0], t[1], t[2]), fmax3(t[3], t[4], t[5]), fmaxf(t[6], t[7])));
+      for (int q = 0; q < kPartPages; ++q) {
+        const float* t = s + kPage * q;
+        const float a = fmax3(t[0], t[1], t[2]), b = fmax3(t[3], t[4], t[5]), c = fmax3(t[6], t[7], t[8]),
+                    d = fmax3(t[9], t[10], t[11]), e = fmax3(t[12], t[13], t[14]);
+        mx = fmaxf(mx, kf[q] * fmaxf(fmax3(a, b, c), fmax3(d, e, t[15])));
       }
-      const float lv_top = fmaxf(fmaxf(lv[0], lv[1]), fmaxf(lv[2], lv[3]));
-      const bool need = mx > m_used + kRescaleLog2;
       const bool gain = lv_top + lg > kGainTop;  // (the same for every row)
-      if (__any_sync(0xffffffffu, need) || gain) {
-        const float m_new = need ? mx : m_used;
-        const float fl = need ? fast_exp2(m_used - m_new) : 1.f;
-        const float lg_new = gain ? kGainTop - 2.f - ceilf(lv_top) : lg;
+      if (!ok) soft_fail[quarter] = 1;
+      if (quarter_any(quarter, mx > m_used + kRescaleLog2 || gain || !ok)) {
+        xch[part * kRowsTC + r] = mx;
+        quarter_sync(quarter);
+        float m_new = m_used;
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) m_new = fmaxf(m_new, xch[q * kRowsTC + r]);
+        const bool fail = soft_fail[quarter] != 0;
+        quarter_sync(quarter);  // (xch and soft_fail are read)
+        if (fail) {
+          ok = false;
+          break;
+        }
+        if (!(m_new > m_used + kRescaleLog2)) m_new = m_used;
+        const float fl = m_new > m_used ? fast_exp2(m_used - m_new) : 1.f;
+        const float lg_new = gain ? kGainTop - 4.f - ceilf(lv_top) : lg;
         const float f = fl * exp2f(lg_new - lg);
-        if (k >= 1) {
-          // O holds this group's earlier tiles: wait for their last P.V, then rescale
-          ok = mbar_wait(&bars[Sm::oDone + grp], (k - 1) & 1);
-          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        if (i >= 1) {
+          // O holds the earlier tiles: wait for their last P.V, then rescale
+          ok = mbar_wait_warp(smem_u32(&bars[Sm::oDone + ((i - 1) & 1)]), ((i - 1) >> 1) & 1);
+          __syncwarp();
           tc::fence_after_sync();
-#pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
+#pragma unroll
+          for (int c = 0; c < DP / 16; ++c) {
             float o[16];
             tc::ld16(tO + 16 * c, o);
 #pragma unroll
@@ -517,88 +583,80 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         m_used = m_new;
         lg = lg_new;
       }
-      // (a group can meet a row's keys only in a later tile: while its max is still -inf,
+      // (a part can meet a row's keys only in a later tile: while its max is still -inf,
       // every probability is 0, not exp2(-inf + inf))
       const float nm = m_used == -CUDART_INF_F ? 0.f : -m_used;
-      const float ginv = exp2f(-lg);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {  // a page's 16 keys -> 8 columns of P, 8 of remainders
+      for (int q = 0; q < kPartPages; ++q) {  // a page's 16 keys -> 8 columns of P, 8 of remainders
         uint32_t h[8], lo[8];
         // (a page of zeros has no say in the gain: its probabilities count with gain 1)
         const bool zero = lv[q] == -CUDART_INF_F;
-        const float off = nm + (zero ? 0.f : lv[q] + lg);
-        const float2 k2 = make_float2(kf[q], kf[q]), o2 = make_float2(off, off);
+        const float up = zero ? 0.f : lv[q] + lg;
+        const float off = nm + up;
+        const float2 kk = make_float2(kf[q], kf[q]), oo = make_float2(off, off);
         float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-          const float2 x = __ffma2_rn(make_float2(s[16 * q + 2 * u], s[16 * q + 2 * u + 1]), k2, o2);
+          const float2 x = __ffma2_rn(make_float2(s[kPage * q + 2 * u], s[kPage * q + 2 * u + 1]), kk, oo);
           const float2 pe = make_float2(fast_exp2(x.x), fast_exp2(x.y));
           sum = u == 0 ? pe : __fadd2_rn(sum, pe);
           split2(pe, h[u], lo[u]);
         }
-        l = fmaf(sum.x + sum.y, zero ? 1.f : iv[q] * ginv, l);
-        tc::st8_nowait(tS + 16 * q, h);
-        tc::st8_nowait(tS + 16 * q + 8, lo);
+        l = fmaf(sum.x + sum.y, fast_exp2(-up), l);
+        tc::st8_nowait(tS + kPage * q, h);
+        tc::st8_nowait(tS + kPage * q + 8, lo);
       }
       tc::st_wait();
       tc::fence_before_sync();
-      mbar_arrive(&bars[Sm::pFull + 2 * grp + (k & 1)]);
+      // (one arrival a warp: arrivals of 512 threads on one barrier are served one by one)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[Sm::pFull + (i & 1)]);
     }
-    if (ok && n_mine > 0) {  // this group's last P.V
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars[Sm::oDone + grp], (n_mine - 1) & 1));
-    }
+    if (ok && i == n_tiles)  // the last P.V
+      ok = mbar_wait_warp(smem_u32(&bars[Sm::oDone + ((n_tiles - 1) & 1)]), ((n_tiles - 1) >> 1) & 1);
+    __syncwarp();
     tc::fence_before_sync();
-    // the two groups' (max, sum, gain) of this row, exchanged once
-    float* xm = xch;  // [group][row] (the queries' maxima are done with)
-    float* xl = xm + 2 * kRowsTC;
-    float* xg = xl + 2 * kRowsTC;  // one value per group and row, as the others
-    xm[grp * kRowsTC + r] = m_used;
-    xl[grp * kRowsTC + r] = l;
-    if (r == 0) xg[grp] = lg;
-    mbar_arrive(&bars[Sm::xfin]);
-    ok = __all_sync(0xffffffffu, mbar_wait(&bars[Sm::xfin], 0) && ok);
-    if (!ok) *abort_flag = 1;
-    if (ok) {
+    // the row's sum over its parts (the maximum and the gain are common)
+    xch[part * kRowsTC + r] = l;
+    if (!ok) soft_fail[quarter] = 1;
+    quarter_sync(quarter);
+    if (soft_fail[quarter]) {
+      *abort_flag = 1;
+    } else {
       tc::fence_after_sync();
-      const float m_o = xm[(grp ^ 1) * kRowsTC + r], l_o = xl[(grp ^ 1) * kRowsTC + r];
-      const float lg_o = xg[grp ^ 1];
-      const float M = fmaxf(m_used, m_o);
-      const float a_me = m_used == -CUDART_INF_F ? 0.f : fast_exp2(m_used - M);
-      const float a_ot = m_o == -CUDART_INF_F ? 0.f : fast_exp2(m_o - M);
-      const float lsum = l * a_me + l_o * a_ot;
+      float lsum = 0.f;
+#pragma unroll
+      for (int q = 0; q < kParts; ++q) lsum += xch[q * kRowsTC + r];
       // a split block leaves its unnormalised partial for the merge
       const bool partial = p.ksplit > 1;
-      const float inv = partial ? 1.f : 1.f / lsum;
-      const float w_me = a_me * inv * exp2f(-lg), w_ot = a_ot * inv * exp2f(-lg_o);
-      const float wA = grp == 0 ? w_me : w_ot, wB = grp == 0 ? w_ot : w_me;
-      const bool hasB = n_tiles > 1;  // group 1's accumulator holds data
+      const float wt = (partial ? 1.f : 1.f / lsum) * exp2f(-lg);
       const size_t pidx = (static_cast<size_t>(tile_index(p, tile, g, b)) * p.ksplit + ks) * kRowsTC + r;
-      float* dst = !valid_row ? nullptr
-                   : partial ? p.ws_o + pidx * D
-                             : p.out + (static_cast<size_t>(q0 + rho / p.G) * p.Hq + g * p.G + rho % p.G) * D;
-      if (partial && valid_row && grp == 0) {
-        p.ws_m[pidx] = M;
+      if (partial && valid_row && part == 0) {
+        p.ws_m[pidx] = m_used;
         p.ws_l[pidx] = lsum;
       }
-      // group grp writes head_dim columns [grp D/2, (grp + 1) D/2) of its row
+      // The row is put together in shared memory (the K and V operands are done with) and
+      // leaves as one bulk copy (the end of a block, last products included: 2.1 us; 3.7 us
+      // with stores of single 16-byte pieces of 32 rows at a time).  Rows are padded by 16
+      // bytes against bank conflicts.
+      uint8_t* const orow = smem + Sm::k0 + r * (D * 4 + 16);
+      __syncwarp();
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        const int col = (D / 2) * grp + 32 * c;
-        float oa[32], ob[32];
-        tc::ld32(tmem + lane_base + col, oa);
-        if (hasB) {
-          tc::ld32(tmem + lane_base + D + col, ob);
-        } else {
+      for (int c = 0; c < DP / 16; ++c) {
+        float o[16];
+        tc::ld16(tO + 16 * c, o);
 #pragma unroll
-          for (int u = 0; u < 32; ++u) ob[u] = 0.f;
-        }
-        if (dst) {
-#pragma unroll
-          for (int u = 0; u < 32; u += 4)
-            *reinterpret_cast<float4*>(dst + col + u) =
-                make_float4(oa[u] * wA + ob[u] * wB, oa[u + 1] * wA + ob[u + 1] * wB,
-                            oa[u + 2] * wA + ob[u + 2] * wB, oa[u + 3] * wA + ob[u + 3] * wB);
-        }
+        for (int u = 0; u < 16; u += 4)
+          *reinterpret_cast<float4*>(orow + (DP * part + 16 * c + u) * 4) =
+              make_float4(o[u] * wt, o[u + 1] * wt, o[u + 2] * wt, o[u + 3] * wt);
+      }
+      fence_proxy_async_smem();
+      quarter_sync(quarter);
+      if (part == 0 && valid_row) {
+        float* dst = partial ? p.ws_o + pidx * D
+                             : p.out + (static_cast<size_t>(q0 + rho / p.G) * p.Hq + g * p.G + rho % p.G) * D;
+        bulk_s2g(dst, orow, D * 4);
+        bulk_store_wait();
       }
     }
   }
@@ -613,22 +671,22 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   if (tid == 0 && err && p.dev_status) atomicOr(p.dev_status, err);
   if (err && valid_row) {
     float* dst = p.out + (static_cast<size_t>(q0 + rho / p.G) * p.Hq + g * p.G + rho % p.G) * D;
-    for (int d = (D / 2) * grp; d < (D / 2) * (grp + 1); ++d) dst[d] = CUDART_NAN_F;
-    if (p.ksplit > 1 && grp == 0)  // a poisoned partial turns the merged row into NaN
+    for (int d = (D / kParts) * part; d < (D / kParts) * (part + 1); ++d) dst[d] = CUDART_NAN_F;
+    if (p.ksplit > 1 && part == 0)  // a poisoned partial turns the merged row into NaN
       p.ws_m[(static_cast<size_t>(tile_index(p, tile, g, b)) * p.ksplit + ks) * kRowsTC + r] = CUDART_NAN_F;
   }
   if (warp == kMmaWarp) tc::tmem_dealloc(tmem, Sm::tmemCols);
   if (p.ksplit > 1) {
     // a block with no key tiles (a short row range split more ways than it has tiles)
     // leaves an empty partial
-    if (n_tiles == 0 && !err && valid_row && grp == 0) {
+    if (n_tiles == 0 && !err && valid_row && part == 0) {
       const size_t pidx = (static_cast<size_t>(tile_index(p, tile, g, b)) * p.ksplit + ks) * kRowsTC + r;
       p.ws_m[pidx] = -CUDART_INF_F;
       p.ws_l[pidx] = 0.f;
       for (int d = 0; d < D; d += 4)
         *reinterpret_cast<float4*>(p.ws_o + pidx * D + d) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    split_merge<D, kThreadsB>(p, tile, g, b, q0, nrows, err, tid, smem + Sm::xch0);
+    split_merge<D, Sm::threads>(p, tile, g, b, q0, nrows, err, tid, smem + Sm::xch0);
   }
 }
 
@@ -638,15 +696,19 @@ const void* blk_kernel() {
 }
 struct BlkVariant {
   const void* fn;
-  int smem;
+  int smem, threads;
 };
+template <int D, bool QSPLIT>
+BlkVariant variant_of(const void* fn) {
+  return {fn, BSmem<D, QSPLIT>::total, BSmem<D, QSPLIT>::threads};
+}
 BlkVariant blk_variant(bool fp8, int D, bool qsplit) {
   if (D == 64) {
-    if (qsplit) return {fp8 ? blk_kernel<true, 64, true>() : blk_kernel<false, 64, true>(), BSmem<64, true>::total};
-    return {fp8 ? blk_kernel<true, 64, false>() : blk_kernel<false, 64, false>(), BSmem<64, false>::total};
+    if (qsplit) return variant_of<64, true>(fp8 ? blk_kernel<true, 64, true>() : blk_kernel<false, 64, true>());
+    return variant_of<64, false>(fp8 ? blk_kernel<true, 64, false>() : blk_kernel<false, 64, false>());
   }
-  if (qsplit) return {fp8 ? blk_kernel<true, 128, true>() : blk_kernel<false, 128, true>(), BSmem<128, true>::total};
-  return {fp8 ? blk_kernel<true, 128, false>() : blk_kernel<false, 128, false>(), BSmem<128, false>::total};
+  if (qsplit) return variant_of<128, true>(fp8 ? blk_kernel<true, 128, true>() : blk_kernel<false, 128, true>());
+  return variant_of<128, false>(fp8 ? blk_kernel<true, 128, false>() : blk_kernel<false, 128, false>());
 }
 
 constexpr int kMaxDevicesB = 64;
@@ -675,7 +737,7 @@ cudaError_t launch_prefill_blk(const PrefillArgs& a, int n_row_tiles, int ksplit
   }
   const dim3 grid(n_row_tiles * ksplit, a.c.Hkv, a.B);
   void* args[] = {const_cast<TParams*>(&p)};
-  return cudaLaunchKernel(v.fn, grid, dim3(kThreadsB), args, v.smem, st);
+  return cudaLaunchKernel(v.fn, grid, dim3(v.threads), args, v.smem, st);
 }
 
 }  // namespace pkv
