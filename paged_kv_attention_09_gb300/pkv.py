@@ -178,8 +178,15 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# the current stream's handle without building a Stream object (a microsecond or two per
+# call), where this torch offers it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
         return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
@@ -236,6 +243,7 @@ class KVCache:
         if self.kv_dtype == INT4:
             self.head_dim *= 2
         self.window = int(window)  # sliding window in tokens (0: none), read by every call
+        self._struct = self._made = None
 
     @classmethod
     def allocate(cls, num_pages, num_kv_heads, head_dim, kv_dtype, device="cuda",
@@ -262,11 +270,15 @@ class KVCache:
                        window=self.window, kv_dtype=self.kv_dtype)
 
     def struct(self) -> pkv_cache:
-        return pkv_cache(self.k.data_ptr(), self.v.data_ptr(),
-                         None if self.k_scale is None else self.k_scale.data_ptr(),
-                         None if self.v_scale is None else self.v_scale.data_ptr(),
-                         self.num_pages, self.page_size, self.num_kv_heads, self.head_dim,
-                         self.kv_dtype, self.window)
+        """The C descriptor: made once and again whenever a tensor or the window changes (a
+        bound call keeps the one it was made with; not to be written to)."""
+        ks, vs = self.k_scale, self.v_scale
+        now = (self.k.data_ptr(), self.v.data_ptr(), None if ks is None else ks.data_ptr(),
+               None if vs is None else vs.data_ptr(), self.num_pages, self.page_size,
+               self.num_kv_heads, self.head_dim, self.kv_dtype, self.window)
+        if now != self._made:
+            self._struct, self._made = pkv_cache(*now), now
+        return self._struct
 
 
 def pkv_status_string(code: int) -> str:
@@ -515,11 +527,6 @@ def _issue(fn, args, what: str, bound: bool, index: int):
     if code != 0:
         raise PkvError(code, what)
     return None
-
-
-# the current stream's handle without building a Stream object (a microsecond or two per
-# call), where this torch offers it
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream_on(stream, index: int) -> int:
