@@ -472,9 +472,9 @@ void pkv_decode_graph_destroy(pkv_decode_graph* graph);
  *
  * The pool.  ring holds page ids; the free ones are the state[1] entries from state[0] on,
  * wrapping at num_pages.  Pages are taken from its front and returned behind its end.  A new
- * pool of N pages is ring = {0 .. N-1} and state = {0, N, 0, 0}.  state[2] is zero between
- * calls (a ticket the call's blocks use); state[3] is not used.  Calls on one pool must be
- * ordered (one stream, or events).
+ * pool of N pages is ring = {0 .. N-1} and state = {0, N, 0, 0}.  state[2] and state[3] are
+ * zero between calls (the call's blocks use them).  Calls on one pool must be ordered (one
+ * stream, or events).
  *
  *   cached_lens    int32 [num_seqs]: tokens of request b already in cache; its block table
  *                  names the pages of those
@@ -497,8 +497,9 @@ void pkv_decode_graph_destroy(pkv_decode_graph* graph);
  * needs some is served while the pages needed up to and with it fit the free ones
  * (else PKV_DEV_NO_PAGES).  Lengths below zero or beyond the table, and rows beyond
  * max_tokens, are not served (PKV_DEV_BAD_LEN); a row whose page id is outside the pool
- * gets slot -1 (PKV_DEV_BAD_PAGE), as does an impossible pool state or a page returned to a
- * full pool.  The pool is untouched by requests that are not served.
+ * gets slot -1 (PKV_DEV_BAD_PAGE, which an impossible pool state also sets, and so do pages
+ * returned beyond the num_pages - free places that were there before the call: those are
+ * dropped).  The pool is untouched by requests that are not served.
  */
 typedef struct pkv_page_pool {
   int32_t* ring;      /* [num_pages] */

@@ -1906,7 +1906,18 @@ bool plan_decode(const CacheView& c, int B, int Hq, int MB, int q_dtype, int dev
     const long long units = static_cast<long long>(B) * c.Hkv * plan->head_groups;
     const long long slots = static_cast<long long>(sms) * occ;
     long long splits = 1;
-    if (units > 0 && 4 * units < 3 * slots) {
+    if (units > 0 && 4 * units < 3 * slots && block_scaled(c.dtype)) {
+      // Block-scaled formats (added later, so the others' plans and sums stay as they are):
+      // as many splits as fill the slots once at full table length, with at least 4 pages
+      // per warp and at most 64 splits.  (us, by this rule and by the one below: 4 ragged
+      // contexts of 32k, heads of 128, 19.1 and 21.0; 32 x 2k 13.2 and 13.9; 8 x 4k 12.5 and
+      // 14.8; 2 x 1k, heads of 64, 8.3 and 10.2.)
+      splits = slots / units;
+      const long long by_len = mb / (4 * v.warps);
+      if (splits > by_len) splits = by_len;
+      if (splits > 64) splits = 64;
+      if (splits < 1) splits = 1;
+    } else if (units > 0 && 4 * units < 3 * slots) {
       splits = (2 * slots + units - 1) / units;
       const long long by_len = mb / (8 * v.warps);
       if (splits > by_len) splits = by_len;

@@ -12,10 +12,11 @@
 // keeps the chunk's offsets in shared memory; its own 1024 rows then find their request by
 // binary search there.  So no block waits for another, whatever the batch, and a single
 // long prompt spreads over as many blocks as a thousand short ones.  The first row of a new
-// page writes the table entry.  The block that takes the last ticket (an atomic, no
-// waiting: every block has read the ring by then) pushes the ended requests' pages and
-// updates the pool, so that a step works on the pool in place and can be replayed from a
-// CUDA graph.
+// page writes the table entry.  The last block also pushes the ended
+// requests' pages: behind the free ones, so that the places written are never those that
+// other blocks read new pages from.  The block that takes the last ticket (an atomic, no
+// waiting: every block has read the pool's state by then) updates the state, so that a step
+// works on the pool in place and can be replayed from a CUDA graph.
 //
 // Bound by latency, not bytes: a 256-request decode step moves 9 KB.
 #include <cuda_runtime.h>
@@ -47,7 +48,7 @@ struct TablesArgs {
   int32_t* positions;  // may be null
   int32_t* slots;
   int32_t* ring;
-  int32_t* state;  // head, free pages, ticket
+  int32_t* state;  // head, free pages, ticket, pages returned
   int32_t* status;
   int B, MB, N, T;
 };
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs a) {
   __shared__ int s_ring[kChunk];    // ring offset of its first new page from the head
   __shared__ int s_back[kChunk];    // end of its returned pages among the chunk's
   __shared__ Sums s_part[kWarps];
-  __shared__ int s_last, s_alloc;
+  __shared__ int s_alloc;
   __shared__ int s_cnt[kBackRounds * kWarps];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int head0 = a.state[0], free0 = a.state[1];
@@ -234,26 +235,12 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs a) {
   }
   if (blockIdx.x == 0 && tid == 0 && a.starts) a.starts[0] = 0;
 
-  // ---- the last block to finish returns pages and updates the pool
-  if (gridDim.x > 1) {
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) s_last = atomicAdd(a.state + 2, 1) == static_cast<int>(gridDim.x) - 1;
-    __syncthreads();
-    if (!s_last) {
-      bits = __reduce_or_sync(0xffffffffu, bits);
-      if (bits && lane == 0 && a.status) atomicOr(a.status, bits);
-      return;
-    }
-    __threadfence();
-  } else {
-    __syncthreads();
-  }
-  const int alloc = s_alloc;
-  const int room = a.N - (count - alloc);  // places for returned pages
+  // ---- the last block's share: pages of ended requests go back
+  const int room = a.N - count;  // places behind the free pages (more pages than that were
+                                 // returned twice)
   const long long tail = static_cast<long long>(head) + count;
   int pushed = 0;
-  if (before.back > 0 && pool_ok) {
+  if (blockIdx.x == gridDim.x - 1 && before.back > 0 && pool_ok) {
     for (int c0 = 0; c0 < a.B; c0 += kChunk) {
       if (a.B > kChunk) {  // (a single chunk's offsets are still in place)
         __syncthreads();
@@ -320,16 +307,25 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesArgs a) {
     }
     pushed = pushed < room ? pushed : room;
   }
-  if (tid == 0) {
-    if (pool_ok) {
-      const long long h = static_cast<long long>(head) + alloc;
-      a.state[0] = static_cast<int>(h >= a.N ? h - a.N : h);
-      a.state[1] = count - alloc + pushed;
-    }
-    a.state[2] = 0;  // the ticket, ready for the next call
-  }
   bits = __reduce_or_sync(0xffffffffu, bits);
   if (bits && lane == 0 && a.status) atomicOr(a.status, bits);
+
+  // ---- the pool's state
+  __syncthreads();
+  if (tid != 0) return;
+  if (gridDim.x > 1) {
+    if (blockIdx.x == gridDim.x - 1) a.state[3] = pushed;
+    __threadfence();
+    if (atomicAdd(a.state + 2, 1) != static_cast<int>(gridDim.x) - 1) return;
+    __threadfence();
+    pushed = *static_cast<volatile int32_t*>(a.state + 3);
+  }
+  if (pool_ok) {
+    const long long h = static_cast<long long>(head) + s_alloc;
+    a.state[0] = static_cast<int>(h >= a.N ? h - a.N : h);
+    a.state[1] = count - s_alloc + pushed;
+  }
+  a.state[2] = a.state[3] = 0;  // ready for the next call
 }
 
 }  // namespace

@@ -63,7 +63,7 @@ def tables(ring, state, cached, new, bt, max_tokens):
                 pos[start + i], slot[start + i] = p, page * PAGE + p % PAGE
             else:
                 status |= BAD_PAGE
-    room = N - (count - alloc)
+    room = N - count
     pushed = 0
     if ok_pool:
         for b in range(B):
@@ -79,8 +79,8 @@ def tables(ring, state, cached, new, bt, max_tokens):
                         pushed += 1
                     else:
                         status |= BAD_PAGE
-    out_state = [(head + alloc) % N, count - alloc + pushed, 0, state[3]] if ok_pool else \
-        [state[0], state[1], 0, state[3]]
+    out_state = [(head + alloc) % N, count - alloc + pushed, 0, 0] if ok_pool else \
+        [state[0], state[1], 0, 0]
     return dict(bt=bt, context=context, starts=starts, positions=pos, slots=slot, ring=ring,
                 state=out_state, status=status)
 
