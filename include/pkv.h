@@ -486,8 +486,8 @@ void pkv_decode_graph_destroy(pkv_decode_graph* graph);
  *   block_tables   int32 [num_seqs][max_blocks_per_seq], in and out: entries of new pages
  *                  are written, the others left as they are
  *   context_lens   int32 [num_seqs], out: cached + new tokens, as the attention calls take
- *                  them; 0 for requests that ended or were not served.  Must not be
- *                  cached_lens or new_lens themselves (PKV_ERR_UNSUPPORTED).
+ *                  them; 0 for requests that ended or were not served.  Must not overlap
+ *                  cached_lens or new_lens (PKV_ERR_UNSUPPORTED).
  *   q_start_loc    int32 [num_seqs + 1], out, or NULL: first row of every request
  *   positions      int32 [max_tokens], out, or NULL: each row's position
  *   slot_mapping   int32 [max_tokens], out: each row's slot, page * 16 + offset
@@ -575,13 +575,15 @@ pkv_status pkv_rope_plan_init(const pkv_rope_params* params, pkv_rope_plan* plan
  *                  same strides) to turn in place, and otherwise not overlapping them
  *   positions      int32 [num_tokens]; a row at a negative position is padding and is not
  *                  read or written
+ *   dev_status     may be NULL; PKV_DEV_TIMEOUT is the only bit (its rows are not written)
  * Any alignment of the rows' element type is taken; 16-byte vectors are used when bases,
  * strides, head_dim and rotary_dim / 2 allow.
  */
 pkv_status pkv_rope(const pkv_rope_plan* plan, const void* q, void* q_out, int64_t q_stride,
                     int64_t q_out_stride, int32_t num_q_heads, const void* k, void* k_out,
                     int64_t k_stride, int64_t k_out_stride, int32_t num_kv_heads, int32_t dtype,
-                    int32_t num_tokens, int32_t head_dim, const int32_t* positions, void* stream);
+                    int32_t num_tokens, int32_t head_dim, const int32_t* positions,
+                    int32_t* dev_status, void* stream);
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char* pkv_status_string(pkv_status status);

@@ -206,8 +206,8 @@ __global__ void __launch_bounds__(kBlockWarps * 32)
     const int first = __shfl_sync(0xffffffffu, slot, lead);
     const long long tok = base - 1 + lead;
     const int page = first / kPage, off = first % kPage;
-    const unsigned follow = __ballot_sync(0xffffffffu, lane >= lead && slot == first + (lane - lead) &&
-                                                           off + (lane - lead) < kPage);
+    const unsigned follow = __ballot_sync(0xffffffffu, lane >= lead && off + (lane - lead) < kPage &&
+                                                           slot == first + (lane - lead));
     const int n = __ffs(~(follow >> lead)) - 1;
     const size_t blk = static_cast<size_t>(page) * Hkv + h;
     uint8_t* const block = (which ? v_cache : k_cache) + blk * kPage * D;
@@ -321,6 +321,7 @@ cudaError_t launch_block(const CacheView& c, void* k, void* v, float* ks, float*
   // one token per warp, 15 of 16 warps only find that they do not lead a run).
   const int group = 2ll * T * c.Hkv <= 152 * 16 ? 1 : 8;
   const long long items = 2ll * ((T + group - 1) / group) * c.Hkv;
+  if (items / kBlockWarps >= 0x7fffffffll) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>((items + kBlockWarps - 1) / kBlockWarps));
   uint8_t* kb = static_cast<uint8_t*>(k);
   uint8_t* vb = static_cast<uint8_t*>(v);

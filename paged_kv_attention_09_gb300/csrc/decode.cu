@@ -698,8 +698,12 @@ struct QuantWarp {
       float qsum = 0.f;  // sum of the operand values exactly as the MMA sees them
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        const float x[4] = {ldexpf(qv[ks].x, -e), ldexpf(qv[ks].y, -e), ldexpf(qv[ks].z, -e),
-                            ldexpf(qv[ks].w, -e)};
+        float x[4] = {ldexpf(qv[ks].x, -e), ldexpf(qv[ks].y, -e), ldexpf(qv[ks].z, -e),
+                      ldexpf(qv[ks].w, -e)};
+        if constexpr (block_scaled(KVT)) {  // (a negative softmax scale turns the query round)
+#pragma unroll
+          for (int h = 0; h < 4; ++h) x[h] = p.scale_log2 < 0.f ? -x[h] : x[h];
+        }
         uint4 f;
         split_h2(x[0], x[1], f.x, f.y);
         split_h2(x[2], x[3], f.z, f.w);
@@ -716,7 +720,7 @@ struct QuantWarp {
       if (c == 0) {
         rowc[r] = ldexpf(p.scale_log2, e - kMulLog2);
         // (never 0: a masked score of -inf has to stay -inf)
-        if constexpr (block_scaled(KVT)) rowc[r] = fmaxf(rowc[r], 1e-37f);
+        if constexpr (block_scaled(KVT)) rowc[r] = fmaxf(fabsf(rowc[r]), 1e-37f);
         rowc[kMaxHeads + r] = ldexpf(kBias, kMulLog2) * qsum;  // K entered as 2^m (kBias + code)
       }
     }

@@ -484,8 +484,9 @@ __global__ void __launch_bounds__(BSmem<D, QSPLIT>::threads, 1)
       // top in [2^(e-1), 2^e): times 2^k, k = 14 - e
       const int e = static_cast<int>((__float_as_uint(top) >> 23) & 0xffu) - 126;
       const int k = min(14 - e, 126);
-      const float f = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
-      rs = ldexpf(p.scale_log2, -k);
+      // (a negative softmax scale turns the query round)
+      const float f = copysignf(__uint_as_float(static_cast<uint32_t>(127 + k) << 23), p.scale_log2);
+      rs = ldexpf(fabsf(p.scale_log2), -k);
       uint8_t* qhi = smem + Sm::q0;
 #pragma unroll
       for (int c = 0; c < N / 8; ++c) {

@@ -50,6 +50,7 @@ struct RopeArgs {
   void* q_out;
   void* k_out;
   const int32_t* pos;
+  int32_t* status;
   long long qs, ks, qos, kos;  // elements from one token to the next
   int Hq, Hk, T, D, rd;
   int tile;    // tokens per block
@@ -136,6 +137,7 @@ __global__ void __launch_bounds__(kThreads) rope_rows_kernel(const __grid_consta
   __syncthreads();  // (the barrier is initialised, too)
   if (!mbar_wait(bar, 0)) {
     (void)mbar_wait(bar, 0);  // no copy may land in the memory of a block that has left
+    if (a.status) atomicOr(a.status, 0x10);  // PKV_DEV_TIMEOUT
     return;
   }
   const int per_token = H * units;
@@ -277,7 +279,7 @@ extern "C" pkv_status pkv_rope(const pkv_rope_plan* plan, const void* q, void* q
                                int64_t q_out_stride, int32_t num_q_heads, const void* k, void* k_out,
                                int64_t k_stride, int64_t k_out_stride, int32_t num_kv_heads, int32_t dtype,
                                int32_t num_tokens, int32_t head_dim, const int32_t* positions,
-                               void* stream) {
+                               int32_t* dev_status, void* stream) {
   PKV_RANGE("pkv_rope");
   if (!plan) return PKV_ERR_NULL;
   if (dtype != PKV_F32 && dtype != PKV_BF16) return PKV_ERR_DTYPE;
@@ -304,7 +306,7 @@ extern "C" pkv_status pkv_rope(const pkv_rope_plan* plan, const void* q, void* q
   const int elt = dtype == PKV_F32 ? 4 : 2, ve = 16 / elt;
   const uintptr_t bases = (num_q_heads ? reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(q_out) : 0) |
                           (num_kv_heads ? reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(k_out) : 0);
-  if (bases % elt || !pkv::aligned4(positions)) return PKV_ERR_ALIGN;
+  if (bases % elt || !pkv::aligned4(positions) || !pkv::aligned4(dev_status)) return PKV_ERR_ALIGN;
   const long long strides = (num_q_heads ? a.qs | a.qos : 0) | (num_kv_heads ? a.ks | a.kos : 0);
   // bulk copies and 16-byte vectors when every row, every head and both halves of the turned
   // columns start on a 16-byte boundary; single elements otherwise
@@ -316,6 +318,7 @@ extern "C" pkv_status pkv_rope(const pkv_rope_plan* plan, const void* q, void* q
   a.q_out = q_out;
   a.k_out = k_out;
   a.pos = positions;
+  a.status = dev_status;
   a.Hq = num_q_heads;
   a.Hk = num_kv_heads;
   a.T = num_tokens;

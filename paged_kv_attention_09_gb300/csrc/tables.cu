@@ -356,8 +356,11 @@ extern "C" pkv_status pkv_batch_tables(const pkv_page_pool* pool, const int32_t*
                         static_cast<const void*>(pool->ring), static_cast<const void*>(pool->state)})
     if (!aligned4(p)) return PKV_ERR_ALIGN;
   // blocks read every request's lengths while others write the outputs
-  if (num_seqs > 0 && (context_lens == cached_lens || context_lens == new_lens))
-    return PKV_ERR_UNSUPPORTED;
+  const long long bytes = 4ll * num_seqs;
+  for (const int32_t* in : {cached_lens, new_lens}) {
+    const long long apart = reinterpret_cast<const char*>(context_lens) - reinterpret_cast<const char*>(in);
+    if (apart < bytes && -apart < bytes) return PKV_ERR_UNSUPPORTED;
+  }
   pkv::TablesArgs a{cached_lens, new_lens,  block_tables, context_lens, q_start_loc,
                     positions,   slot_mapping, pool->ring, pool->state, dev_status,
                     num_seqs,    max_blocks_per_seq, pool->num_pages, max_tokens};

@@ -158,7 +158,7 @@ def bind(path: str):
     lib.pkv_rope_plan_init.argtypes = [ctypes.POINTER(pkv_rope_params),
                                        ctypes.POINTER(pkv_rope_plan)]
     lib.pkv_rope.argtypes = [ctypes.POINTER(pkv_rope_plan), P, P, I64, I64, I32, P, P, I64, I64,
-                             I32, I32, I32, I32, P, P]
+                             I32, I32, I32, I32, P, P, P]
     for fn in ("pkv_batch_tables", "pkv_rope_plan_init", "pkv_rope"):
         getattr(lib, fn).restype = ctypes.c_int
     GD = ctypes.POINTER(pkv_decode_graph_desc)
@@ -605,8 +605,8 @@ def _rope_rows(name: str, x: torch.Tensor, shape: tuple, dtype, index: int) -> i
 
 def pkv_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
              params: RopeParams, q_out: Optional[torch.Tensor] = None,
-             k_out: Optional[torch.Tensor] = None, stream=None,
-             bound: bool = False) -> Optional[BoundCall]:
+             k_out: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None,
+             stream=None, bound: bool = False) -> Optional[BoundCall]:
     """Turns the rows of q [T, Hq, D] and k [T, Hkv, D] (k may be None) at their positions,
     into q_out and k_out or, where those are None, in place; see include/pkv.h.  The rows may
     be views with any token stride."""
@@ -633,7 +633,8 @@ def pkv_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor
             kop, kos = k_out.data_ptr(), _rope_rows("k_out", k_out, shape, dtype, index)
     return _issue(load().pkv_rope,
                   (params._ref, qp, qop, qs, qos, Hq, kp, kop, ks, kos, Hk, _CODE[dtype], T, D,
-                   positions.data_ptr(), _stream_on(stream, index)),
+                   positions.data_ptr(), None if dev_status is None else dev_status.data_ptr(),
+                   _stream_on(stream, index)),
                   "pkv_rope", bound, index)
 
 

@@ -382,6 +382,51 @@ def test_softmax_scale_of_zero_averages(fp8):
     assert np.abs(out[:1].cpu().numpy() - want[4:]).max() <= tol(bc, tables, A)
 
 
+@pytest.mark.parametrize("fp8", FORMATS, ids=IDS)
+def test_negative_softmax_scale(fp8):
+    rng = np.random.default_rng(18)
+    bc, tables = built(rng, [100], 1, 64, fp8)
+    cache = bc.device(pkv)
+    q = torch.from_numpy(rng.standard_normal((5, 4, 64)).astype(np.float32)).cuda()
+    out = torch.empty(5, 4, 64, device="cuda")
+    want, A = R.prefill(bc, q.cpu().numpy(), [0, 5], tables, [100], -0.125)
+    pkv.pkv_prefill_chunk_attn(cache, q, i32([0, 5]), 5, i32(tables), i32([100]), -0.125, out,
+                               pkv.workspace_for(pkv.pkv_prefill_workspace_size(cache, 1, 4, 5, tables.shape[1])))
+    assert np.abs(out.cpu().numpy() - want).max() <= tol(bc, tables, A)
+    pkv.pkv_decode_attn(cache, q[4:], i32(tables), i32([100]), -0.125, out,
+                        pkv.workspace_for(pkv.pkv_decode_workspace_size(cache, 1, 4, tables.shape[1])))
+    assert np.abs(out[:1].cpu().numpy() - want[4:]).max() <= tol(bc, tables, A)
+
+
+@pytest.mark.parametrize("fp8", FORMATS, ids=IDS)
+def test_offsets_past_32_bits(fp8):
+    """Pages at the far end of a pool whose K alone is larger than 4 GiB: byte offsets of 33
+    bits in append, decode and prefill."""
+    P, H, D = 160000, 16, 128  # 160000 * 16 * 2048 bytes = 5.2 GB for K and as much for V
+    cache = pkv.KVCache.allocate(P, H, D, pkv.FP8B if fp8 else pkv.INT8B)
+    rng = np.random.default_rng(19)
+    table = [P - 1, 3, P - 7]
+    n = 40
+    k, v = draw_rows(rng, n, H, D, torch.float32, 0.3)
+    slots = token_slots(np.array(table), 0, n)
+    assert append(cache, k, v, slots, torch.float32) == 0
+    small = R.BlockCache(3, H, D, fp8)
+    assert small.append(k, v, list(range(n))) == 0
+    for i, page in enumerate(table):
+        assert np.array_equal(cache.k[page].cpu().numpy(), small.k[i]) and np.array_equal(cache.v[page].cpu().numpy(), small.v[i])
+    bt = np.array([table], dtype=np.int32)
+    order = np.array([[0, 1, 2]], dtype=np.int32)
+    q = torch.from_numpy(rng.standard_normal((2, H, D)).astype(np.float32)).cuda()
+    want, A = R.prefill(small, q.cpu().numpy(), [0, 2], order, [n], D ** -0.5)
+    out = torch.empty(2, H, D, device="cuda")
+    pkv.pkv_prefill_chunk_attn(cache, q, i32([0, 2]), 2, i32(bt), i32([n]), D ** -0.5, out,
+                               pkv.workspace_for(pkv.pkv_prefill_workspace_size(cache, 1, H, 2, 3)))
+    assert np.abs(out.cpu().numpy() - want).max() <= tol(small, order, A)
+    pkv.pkv_decode_attn(cache, q[1:], i32(bt), i32([n]), D ** -0.5, out,
+                        pkv.workspace_for(pkv.pkv_decode_workspace_size(cache, 1, H, 3)))
+    assert np.abs(out[:1].cpu().numpy() - want[1:]).max() <= tol(small, order, A)
+
+
 # ------------------------------------------------------------------- graphs and refusals
 
 @pytest.mark.parametrize("fp8", FORMATS, ids=IDS)

@@ -38,7 +38,9 @@ def test_batch_tables_refusals(lib):
         assert _tables(lib, **{name: None}) == 1, name
     for name in ("cached", "new", "bt", "ctx", "qsl", "pos", "slots", "status", "ring", "state"):
         assert _tables(lib, **{name: 0x30002}) == 5, name
-    assert _tables(lib, ctx=0x30000) == 7 and _tables(lib, ctx=0x40000) == 7  # lengths overwritten while read
+    # lengths overwritten while they are read: the same buffer, or one that overlaps it
+    assert _tables(lib, ctx=0x30000) == 7 and _tables(lib, ctx=0x40000) == 7
+    assert _tables(lib, ctx=0x30004) == 7 and _tables(lib, ctx=0x3fffc) == 7 and _tables(lib, cached=0x60004) == 7
 
 
 def _params(**kw):
@@ -73,9 +75,9 @@ def test_rope_call_refusals(lib):
     assert lib.pkv_rope_plan_init(ctypes.byref(_params()), ctypes.byref(plan)) == 0
 
     def call(q=0x10000, qo=0x20000, qs=0, qos=0, hq=4, k=0x30000, ko=0x40000, ks=0, kos=0, hk=2, dt=0, n=3, d=64,
-             pos=0x50000, p=plan):
+             pos=0x50000, p=plan, status=None):
         return lib.pkv_rope(ctypes.byref(p) if p is not None else None, q, qo, qs, qos, hq, k, ko, ks, kos, hk, dt, n, d,
-                            pos, None)
+                            pos, status, None)
     assert call(p=None) == 1
     assert call(dt=2) == 3
     assert call(n=-1) == 2 and call(hq=-1) == 2 and call(hk=-1) == 2 and call(hq=65535, hk=1) == 2
@@ -84,7 +86,7 @@ def test_rope_call_refusals(lib):
     assert call(qs=100) == 2 and call(kos=100) == 2 and call(qs=-512) == 2   # shorter than a row
     assert call(q=None) == 1 and call(ko=None) == 1 and call(pos=None) == 1
     assert call(qo=0x10000, qs=512, qos=1024) == 2   # in place at two strides
-    assert call(q=0x10002) == 5 and call(pos=0x50001) == 5
+    assert call(q=0x10002) == 5 and call(pos=0x50001) == 5 and call(status=0x60002) == 5
     assert call(n=0, q=None, k=None, pos=None) == 0 and call(hq=0, hk=0) == 0
 
 
