@@ -96,8 +96,11 @@ struct BSmem {
   static constexpr int scSlot = 2 * kPagesB * 4;
   static constexpr int bar0 = sc0 + kScaleSlots * scSlot;
   // barriers by index
-  static constexpr int kFull = 0, kEmpty = 2, vFull = 4, vEmpty = 8, sFull = 12, pFull = 15, oDone = 17,
-                       fin = 19, qFull = 20, rawFull = 21, nbars = rawFull + kKWarps + VW;
+  static constexpr int kFull = 0, kEmpty = 2, vFull = 4, vEmpty = 8, sFull = 12, pFull = 15, oDone = 18,
+                       fin = 21, qFull = 22, rawFull = 23, nbars = rawFull + kKWarps + VW;
+  // (A wait by parity tells a phase only from the one before it.  sFull, pFull and oDone are one
+  // barrier per score buffer: S(i + 3) waits for the products of tile i, so that on each of them
+  // whoever waits for tile i does so after tile i - 3 and before tile i + 3.)
   static constexpr int misc0 = bar0 + (nbars + nbars % 2) * 8;  // TMEM base address, abort flag; failed waits of the softmax quarters
   // row values exchanged by the softmax threads [part][row]; then the split merge's weights
   static constexpr int xch0 = misc0 + 32;
@@ -232,7 +235,7 @@ __global__ void __launch_bounds__(BSmem<D, QSPLIT>::threads, 1)
   if (tid == 0) {
     for (int i = 0; i < Sm::nbars; ++i) {
       const int count = i >= Sm::kFull && i < Sm::kFull + Sm::KST     ? 2   // its halves
-                        : i == Sm::pFull || i == Sm::pFull + 1 || i == Sm::qFull ? kSoftWarps
+                        : (i >= Sm::pFull && i < Sm::pFull + kScores) || i == Sm::qFull ? kSoftWarps
                         : i == Sm::fin                                ? 2  // one from each MMA issuer
                                                                       : 1;
       mbar_init(&bars[i], count);
@@ -384,14 +387,14 @@ __global__ void __launch_bounds__(BSmem<D, QSPLIT>::threads, 1)
       const uint64_t dQlo = tc::smem_desc(sbase + Sm::q0 + Sm::qTile, 128, sboQK);
       const uint64_t dK0 = tc::smem_desc(sbase + Sm::k0, 128, sboQK);
       const uint64_t dV0 = tc::smem_desc(sbase + Sm::v0, 128, 256);
-      auto done_bar = [&](int i) { return &bars[Sm::oDone + (i & 1)]; };
+      auto done_bar = [&](int i) { return &bars[Sm::oDone + i % kScores]; };
       bool ok = true;
       if (warp == kMmaWarp) {
         // S of tile i, once its K is there and the last readers of its buffer, the P.V products
         // of tile i - 3, have completed
         ok = mbar_wait(&bars[Sm::qFull], 0);
         for (int i = 0; i < n_tiles && ok; ++i) {
-          ok = (i < kScores || mbar_wait(done_bar(i - kScores), ((i - kScores) >> 1) & 1)) &&
+          ok = (i < kScores || mbar_wait(done_bar(i - kScores), ((i - kScores) / kScores) & 1)) &&
                mbar_wait(&bars[Sm::kFull + i % Sm::KST], (i / Sm::KST) & 1) && !*abort_flag;
           if (!ok) break;
           tc::fence_after_sync();
@@ -411,7 +414,7 @@ __global__ void __launch_bounds__(BSmem<D, QSPLIT>::threads, 1)
         for (int i = 0; i < n_tiles && ok; ++i) {
           for (int h = 2 * i; h < 2 * i + 2 && ok; ++h)
             ok = mbar_wait(&bars[Sm::vFull + h % Sm::VST], (h / Sm::VST) & 1);
-          ok = ok && mbar_wait(&bars[Sm::pFull + (i & 1)], (i >> 1) & 1) && !*abort_flag;
+          ok = ok && mbar_wait(&bars[Sm::pFull + i % kScores], (i / kScores) & 1) && !*abort_flag;
           if (!ok) break;
           tc::fence_after_sync();
           const uint32_t tP = tmem + Sm::sCol + kKeysB * (i % kScores);
@@ -429,8 +432,6 @@ __global__ void __launch_bounds__(BSmem<D, QSPLIT>::threads, 1)
             }
             tc::commit(&bars[Sm::vEmpty + st]);
           }
-          // (two barriers in turn: whoever waits for one of tile i's products may come after
-          // those of tile i + 1 have completed)
           tc::commit(done_bar(i));
         }
       }
@@ -568,7 +569,7 @@ __global__ void __launch_bounds__(BSmem<D, QSPLIT>::threads, 1)
         const float f = fl * exp2f(lg_new - lg);
         if (i >= 1) {
           // O holds the earlier tiles: wait for their last P.V, then rescale
-          ok = mbar_wait_warp(smem_u32(&bars[Sm::oDone + ((i - 1) & 1)]), ((i - 1) >> 1) & 1);
+          ok = mbar_wait_warp(smem_u32(&bars[Sm::oDone + (i - 1) % kScores]), ((i - 1) / kScores) & 1);
           __syncwarp();
           tc::fence_after_sync();
 #pragma unroll
@@ -611,10 +612,10 @@ __global__ void __launch_bounds__(BSmem<D, QSPLIT>::threads, 1)
       tc::fence_before_sync();
       // (one arrival a warp: arrivals of 512 threads on one barrier are served one by one)
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[Sm::pFull + (i & 1)]);
+      if (lane == 0) mbar_arrive(&bars[Sm::pFull + i % kScores]);
     }
     if (ok && i == n_tiles)  // the last P.V
-      ok = mbar_wait_warp(smem_u32(&bars[Sm::oDone + ((n_tiles - 1) & 1)]), ((n_tiles - 1) >> 1) & 1);
+      ok = mbar_wait_warp(smem_u32(&bars[Sm::oDone + (n_tiles - 1) % kScores]), ((n_tiles - 1) / kScores) & 1);
     __syncwarp();
     tc::fence_before_sync();
     // the row's sum over its parts (the maximum and the gain are common)

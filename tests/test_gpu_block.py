@@ -324,6 +324,37 @@ def test_prefill_long_prefix(fp8):
 
 
 @pytest.mark.parametrize("fp8", FORMATS, ids=IDS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_prefill_reads_from_cold_memory(fp8, D, dtype):
+    """With the cache out of L2 the softmax can be three tiles ahead of the values: every call
+    gives the same bits, over one to fourteen key tiles and their shares."""
+    rng = np.random.default_rng(D)
+    lens, chunk = [100, 230, 380, 500, 640, 1290, 1700], 24
+    starts = np.arange(len(lens) + 1) * chunk
+    bc, tables = built(rng, lens, 1, D, fp8, spread=0.5)
+    q = torch.from_numpy(rng.standard_normal((starts[-1], 5, D)).astype(np.float32)).to(dtype).cuda()
+    want, A = R.prefill(bc, q.float().cpu().numpy(), starts, tables, lens, 1 / np.sqrt(D))
+    other = torch.empty(512 << 20, dtype=torch.uint8, device="cuda")
+    cache = bc.device(pkv)
+    for key_split in (1, 2, 3):
+        n = pkv.pkv_prefill_workspace_size(cache, len(lens), 5, chunk, tables.shape[1], key_split)
+        ws = pkv.workspace_for(n)
+        first = None
+        for _ in range(8):
+            out = torch.full(q.shape, 7.0, device="cuda")
+            status = torch.zeros(1, dtype=torch.int32, device="cuda")
+            other.add_(1)
+            pkv.pkv_prefill_chunk_attn(cache, q, i32(starts), chunk, i32(tables), i32(lens), 1 / np.sqrt(D), out, ws,
+                                       status, key_split=key_split)
+            assert int(status.item()) == 0
+            if first is None:
+                first = out
+                assert np.abs(out.cpu().numpy() - want).max() <= tol(bc, tables, A), key_split
+            assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("fp8", FORMATS, ids=IDS)
 @pytest.mark.parametrize("key_split", [1, 3])
 def test_prefill_reports_errors(fp8, key_split):
     rng = np.random.default_rng(12)
