@@ -20,22 +20,22 @@
 //                150 cycles in this kernel, so a page's loads are in flight together and every
 //                wait, fence and arrival stands for 64 keys: one page a time and warp, each with
 //                its own, took 2700 cycles a page;
-//   warp 16      one thread issues S(i) = Q K^T (M = 128, N = 128) into one of three score
-//                buffers of TMEM, warp 17 one thread O += P(i) V (M = 128, N = head_dim):
+//   warp 16      one thread issues S(i) = Q K^T (M = 128, N = 128) into one of two (head_dim 64:
+//                three) score buffers of TMEM, warp 17 one thread O += P(i) V (M = 128, N = head_dim):
 //                two issuers, since each barrier that one asks costs it as much as two MMAs;
 //   warps 0-15   softmax, four threads per row, 32 keys each.  They share the row's running
 //                maximum: it is raised only when a score passes it by 2^8, so nearly every
 //                tile costs the four warps of 32 rows one barrier with a vote, not an exchange.  P overwrites
 //                its own scores in TMEM, page by page (8 columns of FP16 high parts, 8 of
-//                remainders: P keeps ~22 bits, two MMAs per page), so that three score
-//                buffers fit beside the accumulator.
-// What bounds it: a tile takes ~2400 cycles, of which the softmax's exponentials take 1024 on
+//                remainders: P keeps ~22 bits, two MMAs per page), so that the score buffers
+//                fit beside O and the sum of its earlier segments (kSegment).
+// What bounds it: a tile takes ~2500 cycles, of which the softmax's exponentials take 1024 on
 // the special-function pipe; they do not overlap with the same warps' loads, votes and waits
 // (~1300), since the four warps of a scheduler are the four parts of the same rows.  The MMAs
 // take 1600 and the fills less.  Measured (cycles a tile; 4 x 512 tokens over 4096, 12 / 2 heads
 // of 128, FP8B): 4400 with the codes through registers or asynchronous copies and one MMA
 // issuer, 3300 with whole runs of 64 keys per warp and no bank conflicts, 2600 with two issuers.
-// That workload: 52.0 us, 655 TFLOP/s; 2 chunks of 512 over 2048: 33.6 us.
+// That workload: 55.0 us, 618 TFLOP/s; 2 chunks of 512 over 2048: 35.1 us.
 //
 // Range of FP16: query rows are brought to [2^13, 2^14) by a power of two that goes into the
 // score scale (float queries as high part + remainder); probabilities carry the V scale as
@@ -66,7 +66,12 @@ constexpr int kVWarp = kKWarp + kKWarps;
 constexpr int kKeysB = 128;               // keys per tile
 constexpr int kPagesB = kKeysB / kPage;
 constexpr int kPartKeys = kKeysB / kParts, kPartPages = kPagesB / kParts;
-constexpr int kScores = 3;               // score buffers
+// Key tiles whose products one accumulator takes.  The tensor core adds with truncation: over n
+// additions a sum loses about n 2^-25 of itself, and a tile adds 16 times.  (Error of 512 rows over
+// 2048 keys, relative, and time of 4 x 512 over 4096: segments of 2 tiles 0.4e-6, 57.0 us; 4 tiles
+// 0.8e-6, 55.0; 8 tiles 1.7e-6, 54.1; one accumulator 4.3e-6, 52.9.  A sum in FP32 with rounding,
+// key by key: 0.9e-6.)
+constexpr int kSegment = 4;
 constexpr int kScaleSlots = 8;
 constexpr float kGainTop = 7.f;          // log2 of the largest scaled V scale
 
@@ -80,6 +85,7 @@ struct BSmem {
   static constexpr int blk = kPage * D * 2;          // one FP16 page block (K or V)
   static constexpr int qTile = kRowsTC * D * 2;      // one FP16 query tile
   static constexpr int half = kPagesTC * blk;        // operand blocks of 64 keys
+  static constexpr int SB = D == 128 ? 2 : 3;        // score buffers
   static constexpr int KST = 2;                      // K ring: tiles
   static constexpr int VST = QSPLIT ? 3 : 4;         // V ring: halves
   static constexpr int VW = QSPLIT ? 2 : 3;          // warps that fill the V ring
@@ -99,16 +105,17 @@ struct BSmem {
   static constexpr int kFull = 0, kEmpty = 2, vFull = 4, vEmpty = 8, sFull = 12, pFull = 15, oDone = 18,
                        fin = 21, qFull = 22, rawFull = 23, nbars = rawFull + kKWarps + VW;
   // (A wait by parity tells a phase only from the one before it.  sFull, pFull and oDone are one
-  // barrier per score buffer: S(i + 3) waits for the products of tile i, so that on each of them
-  // whoever waits for tile i does so after tile i - 3 and before tile i + 3.)
+  // barrier per score buffer: S(i + SB) waits for the products of tile i, so that on each of
+  // them whoever waits for tile i does so after tile i - SB and before tile i + SB.)
   static constexpr int misc0 = bar0 + (nbars + nbars % 2) * 8;  // TMEM base address, abort flag; failed waits of the softmax quarters
   // row values exchanged by the softmax threads [part][row]; then the split merge's weights
   static constexpr int xch0 = misc0 + 32;
   static constexpr int total = xch0 + kParts * kRowsTC * 4;
-  // TMEM columns: O [0, D), score buffer i at 128 + 128 i (part h's 32 keys at + 32 h)
-  static constexpr int sCol = 128;
+  // TMEM columns: O [0, D), the earlier segments' sum [D, 2 D), then score buffers of 128
+  // columns (part h's 32 keys at + 32 h)
+  static constexpr int tCol = D, sCol = 2 * D;
   static constexpr int tmemCols = 512;
-  static_assert(sCol + kScores * kKeysB <= 512 && D <= sCol, "tensor memory");
+  static_assert(sCol + SB * kKeysB <= 512, "tensor memory");
   static_assert(total <= 227 * 1024, "shared memory");
 };
 
@@ -235,7 +242,7 @@ __global__ void __launch_bounds__(BSmem<D, QSPLIT>::threads, 1)
   if (tid == 0) {
     for (int i = 0; i < Sm::nbars; ++i) {
       const int count = i >= Sm::kFull && i < Sm::kFull + Sm::KST     ? 2   // its halves
-                        : (i >= Sm::pFull && i < Sm::pFull + kScores) || i == Sm::qFull ? kSoftWarps
+                        : (i >= Sm::pFull && i < Sm::pFull + Sm::SB) || i == Sm::qFull ? kSoftWarps
                         : i == Sm::fin                                ? 2  // one from each MMA issuer
                                                                       : 1;
       mbar_init(&bars[i], count);
@@ -387,26 +394,26 @@ __global__ void __launch_bounds__(BSmem<D, QSPLIT>::threads, 1)
       const uint64_t dQlo = tc::smem_desc(sbase + Sm::q0 + Sm::qTile, 128, sboQK);
       const uint64_t dK0 = tc::smem_desc(sbase + Sm::k0, 128, sboQK);
       const uint64_t dV0 = tc::smem_desc(sbase + Sm::v0, 128, 256);
-      auto done_bar = [&](int i) { return &bars[Sm::oDone + i % kScores]; };
+      auto done_bar = [&](int i) { return &bars[Sm::oDone + i % Sm::SB]; };
       bool ok = true;
       if (warp == kMmaWarp) {
         // S of tile i, once its K is there and the last readers of its buffer, the P.V products
-        // of tile i - 3, have completed
+        // of tile i - SB, have completed
         ok = mbar_wait(&bars[Sm::qFull], 0);
         for (int i = 0; i < n_tiles && ok; ++i) {
-          ok = (i < kScores || mbar_wait(done_bar(i - kScores), ((i - kScores) / kScores) & 1)) &&
+          ok = (i < Sm::SB || mbar_wait(done_bar(i - Sm::SB), ((i - Sm::SB) / Sm::SB) & 1)) &&
                mbar_wait(&bars[Sm::kFull + i % Sm::KST], (i / Sm::KST) & 1) && !*abort_flag;
           if (!ok) break;
           tc::fence_after_sync();
           const uint64_t dK = tc::desc_add(dK0, (i % Sm::KST) * 2 * Sm::half);
-          const uint32_t tS = tmem + Sm::sCol + kKeysB * (i % kScores);
+          const uint32_t tS = tmem + Sm::sCol + kKeysB * (i % Sm::SB);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint64_t bd = tc::desc_add(dK, k * 256);
             tc::mma_bf16(tS, tc::desc_add(dQhi, k * 256), bd, idS, k > 0);
             if constexpr (QSPLIT) tc::mma_bf16(tS, tc::desc_add(dQlo, k * 256), bd, idS, true);
           }
-          tc::commit(&bars[Sm::sFull + i % kScores]);
+          tc::commit(&bars[Sm::sFull + i % Sm::SB]);
           tc::commit(&bars[Sm::kEmpty + i % Sm::KST]);
         }
       } else {
@@ -414,10 +421,10 @@ __global__ void __launch_bounds__(BSmem<D, QSPLIT>::threads, 1)
         for (int i = 0; i < n_tiles && ok; ++i) {
           for (int h = 2 * i; h < 2 * i + 2 && ok; ++h)
             ok = mbar_wait(&bars[Sm::vFull + h % Sm::VST], (h / Sm::VST) & 1);
-          ok = ok && mbar_wait(&bars[Sm::pFull + i % kScores], (i / kScores) & 1) && !*abort_flag;
+          ok = ok && mbar_wait(&bars[Sm::pFull + i % Sm::SB], (i / Sm::SB) & 1) && !*abort_flag;
           if (!ok) break;
           tc::fence_after_sync();
-          const uint32_t tP = tmem + Sm::sCol + kKeysB * (i % kScores);
+          const uint32_t tP = tmem + Sm::sCol + kKeysB * (i % Sm::SB);
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             const int st = (2 * i + y) % Sm::VST;
@@ -428,7 +435,7 @@ __global__ void __launch_bounds__(BSmem<D, QSPLIT>::threads, 1)
 #pragma unroll
               for (int half = 0; half < 2; ++half)
                 tc::mma_bf16_ts(tmem, tP + 16 * (kPagesTC * y + q) + 8 * half, bd, idO,
-                                !(i == 0 && y == 0 && q == 0 && half == 0));
+                                !(i % kSegment == 0 && y == 0 && q == 0 && half == 0));
             }
             tc::commit(&bars[Sm::vEmpty + st]);
           }
@@ -508,7 +515,7 @@ __global__ void __launch_bounds__(BSmem<D, QSPLIT>::threads, 1)
     const int lo_row = win > 0 ? pos - win + 1 : 0;  // first key of the row's window
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     constexpr int DP = D / kParts;  // columns of O that this thread rescales and writes
-    const uint32_t tO = tmem + lane_base + DP * part;
+    const uint32_t tO = tmem + lane_base + DP * part, tT = tO + Sm::tCol;
     float m_used = -CUDART_INF_F, l = 0.f;
     float lg = 100.f;  // log2 of the gain on the V scales (the first tile brings it down)
     bool ok = true;
@@ -516,12 +523,12 @@ __global__ void __launch_bounds__(BSmem<D, QSPLIT>::threads, 1)
     // gave up only raises soft_fail, which all of them see in the same tile.
     int i = 0;
     for (; i < n_tiles; ++i) {
-      ok = mbar_wait_warp(smem_u32(&bars[Sm::sFull + i % kScores]), (i / kScores) & 1) && ok;
+      ok = mbar_wait_warp(smem_u32(&bars[Sm::sFull + i % Sm::SB]), (i / Sm::SB) & 1) && ok;
 #ifdef PKV_TEST_HOOKS
       if (i == 0 && g_test_prefill_blk_fail_first_wait) ok = false;  // a wait that gives up
 #endif
       tc::fence_after_sync();
-      const uint32_t tS = tmem + lane_base + Sm::sCol + kKeysB * (i % kScores) + kPartKeys * part;
+      const uint32_t tS = tmem + lane_base + Sm::sCol + kKeysB * (i % Sm::SB) + kPartKeys * part;
       const float* sc = reinterpret_cast<const float*>(smem + Sm::sc0 + (i % kScaleSlots) * Sm::scSlot);
       const float2 k2 = *reinterpret_cast<const float2*>(sc + kPartPages * part);
       const float2 v2 = *reinterpret_cast<const float2*>(sc + kPagesB + kPartPages * part);
@@ -569,7 +576,7 @@ __global__ void __launch_bounds__(BSmem<D, QSPLIT>::threads, 1)
         const float f = fl * exp2f(lg_new - lg);
         if (i >= 1) {
           // O holds the earlier tiles: wait for their last P.V, then rescale
-          ok = mbar_wait_warp(smem_u32(&bars[Sm::oDone + (i - 1) % kScores]), ((i - 1) / kScores) & 1);
+          ok = mbar_wait_warp(smem_u32(&bars[Sm::oDone + (i - 1) % Sm::SB]), ((i - 1) / Sm::SB) & 1);
           __syncwarp();
           tc::fence_after_sync();
 #pragma unroll
@@ -579,6 +586,12 @@ __global__ void __launch_bounds__(BSmem<D, QSPLIT>::threads, 1)
 #pragma unroll
             for (int u = 0; u < 16; ++u) o[u] *= f;
             tc::st16(tO + 16 * c, o);
+            if (i > kSegment) {
+              tc::ld16(tT + 16 * c, o);
+#pragma unroll
+              for (int u = 0; u < 16; ++u) o[u] *= f;
+              tc::st16(tT + 16 * c, o);
+            }
           }
         }
         l *= fl;
@@ -609,13 +622,31 @@ __global__ void __launch_bounds__(BSmem<D, QSPLIT>::threads, 1)
         tc::st8_nowait(tS + kPage * q + 8, lo);
       }
       tc::st_wait();
+      if (i > 0 && i % kSegment == 0) {
+        // a segment ends: its accumulator joins the sum of the earlier ones
+        ok = mbar_wait_warp(smem_u32(&bars[Sm::oDone + (i - 1) % Sm::SB]), ((i - 1) / Sm::SB) & 1) && ok;
+        __syncwarp();
+        tc::fence_after_sync();
+#pragma unroll
+        for (int c = 0; c < DP / 16; ++c) {
+          float o[16];
+          tc::ld16(tO + 16 * c, o);
+          if (i > kSegment) {
+            float t[16];
+            tc::ld16(tT + 16 * c, t);
+#pragma unroll
+            for (int u = 0; u < 16; ++u) o[u] += t[u];
+          }
+          tc::st16(tT + 16 * c, o);
+        }
+      }
       tc::fence_before_sync();
       // (one arrival a warp: arrivals of 512 threads on one barrier are served one by one)
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[Sm::pFull + i % kScores]);
+      if (lane == 0) mbar_arrive(&bars[Sm::pFull + i % Sm::SB]);
     }
     if (ok && i == n_tiles)  // the last P.V
-      ok = mbar_wait_warp(smem_u32(&bars[Sm::oDone + (n_tiles - 1) % kScores]), ((n_tiles - 1) / kScores) & 1);
+      ok = mbar_wait_warp(smem_u32(&bars[Sm::oDone + (n_tiles - 1) % Sm::SB]), ((n_tiles - 1) / Sm::SB) & 1);
     __syncwarp();
     tc::fence_before_sync();
     // the row's sum over its parts (the maximum and the gain are common)
@@ -647,6 +678,12 @@ __global__ void __launch_bounds__(BSmem<D, QSPLIT>::threads, 1)
       for (int c = 0; c < DP / 16; ++c) {
         float o[16];
         tc::ld16(tO + 16 * c, o);
+        if (n_tiles > kSegment) {
+          float t[16];
+          tc::ld16(tT + 16 * c, t);
+#pragma unroll
+          for (int u = 0; u < 16; ++u) o[u] += t[u];
+        }
 #pragma unroll
         for (int u = 0; u < 16; u += 4)
           *reinterpret_cast<float4*>(orow + (DP * part + 16 * c + u) * 4) =

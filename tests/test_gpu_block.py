@@ -355,6 +355,34 @@ def test_prefill_reads_from_cold_memory(fp8, D, dtype):
 
 
 @pytest.mark.parametrize("fp8", FORMATS, ids=IDS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_prefill_scores_and_values_that_rise(fp8, D, dtype):
+    """The running maximum and the gain on the values change in the middle and at the ends of
+    the segments that one accumulator takes: what came before keeps its weight."""
+    rng = np.random.default_rng(D + 1)
+    levels = [0, 0, 0, 9, 18, 18, 18, 18, 27.5, 36, 36, 36, 36, 45, 45]  # log2 units, by 128 keys
+    rises = [1, 1, 1, 1, 300, 300, 1, 1e4, 1e4, 1e4, 1e4, 1, 3e5, 3e5, 3e5]
+    n, rows = 128 * len(levels) - 37, 9
+    bc, tables = built(rng, [1], 1, D, fp8, P=R.pages(n) + 2, MB=R.pages(n) + 1)
+    tables[0, :R.pages(n)] = rng.permutation(bc.P)[:R.pages(n)]
+    way = rng.choice([-1.0, 1.0], D)
+    level = np.repeat(levels, 128)[:n, None, None] + 0.5 * rng.standard_normal((n, 1, 1))
+    k = (way * level * np.log(2) / np.sqrt(D)).astype(np.float32)
+    v = (np.repeat(rises, 128)[:n, None, None] * rng.standard_normal((n, 1, D))).astype(np.float32)
+    for t in range(0, n, 16):
+        assert bc.append(k[t:t + 16], v[t:t + 16], token_slots(tables[0], t, min(t + 16, n))) == 0
+    q = torch.from_numpy(np.tile(way, (rows, 4, 1)).astype(np.float32)).to(dtype).cuda()
+    for length in (128 * 5 - 3, 128 * 9 + 30, n):
+        want, A = R.prefill(bc, q.float().cpu().numpy(), [0, rows], tables, [length], 1 / np.sqrt(D))
+        seen = R.block_values(bc.v, bc.fp8) * bc.vs[:, :, None, None]
+        bound = tol(bc, tables, A) / vmax(bc) * np.nanmax(np.abs(seen[tables[0, :R.pages(length)]]))
+        for key_split in (1, 2, 3):
+            got, status = run_prefill(bc, tables, [length], q, [0, rows], key_split=key_split)
+            assert status == 0 and np.abs(got - want).max() <= bound, (length, key_split)
+
+
+@pytest.mark.parametrize("fp8", FORMATS, ids=IDS)
 @pytest.mark.parametrize("key_split", [1, 3])
 def test_prefill_reports_errors(fp8, key_split):
     rng = np.random.default_rng(12)
