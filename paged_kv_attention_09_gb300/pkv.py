@@ -290,10 +290,29 @@ def _opts(split_pages: int):
     return None if not split_pages else ctypes.byref(pkv_decode_opts(int(split_pages)))
 
 
+def _rows_in(cache: KVCache, k_new, v_new, slots) -> None:
+    """New rows of a block-scaled cache: dense, alike, one for each slot."""
+    n = slots.shape[0] * cache.num_kv_heads * cache.head_dim
+    if k_new.dtype is not v_new.dtype or k_new.numel() != n or v_new.numel() != n or \
+            not (k_new.is_contiguous() and v_new.is_contiguous()):
+        raise ValueError("pkv_append: contiguous k_new and v_new [tokens, kv heads, head_dim] of one "
+                         "type are wanted, a row for each slot")
+
+
+def _rows_out(cache: KVCache, q, out, what: str) -> None:
+    """Query and output rows over a block-scaled cache: dense, of the cache's head_dim."""
+    if q.shape[2] != cache.head_dim or out.dtype is not torch.float32 or out.numel() < q.numel() or \
+            not (q.is_contiguous() and out.is_contiguous()):
+        raise ValueError(f"{what}: contiguous q [rows, heads, head_dim] and a float32 out of its shape "
+                         "are wanted")
+
+
 def pkv_append(cache: KVCache, k_new: torch.Tensor, v_new: torch.Tensor,
                slot_mapping: torch.Tensor, dev_status: Optional[torch.Tensor] = None,
                stream=None, bound: bool = False) -> Optional[BoundCall]:
     c = cache.struct()
+    if cache.kv_dtype in BLOCK_SCALED:
+        _rows_in(cache, k_new, v_new, slot_mapping)
     return _call(load().pkv_append,
                  (ctypes.byref(c), _ptr(k_new), _ptr(v_new), _CODE[k_new.dtype],
                   _ptr(slot_mapping), int(slot_mapping.shape[0]), _ptr(dev_status),
@@ -320,6 +339,8 @@ def pkv_decode_attn(cache: KVCache, q: torch.Tensor, block_tables: torch.Tensor,
                     split_pages: int = 0, bound: bool = False) -> Optional[BoundCall]:
     c = cache.struct()
     B, Hq, _ = q.shape
+    if cache.kv_dtype in BLOCK_SCALED:
+        _rows_out(cache, q, out, "pkv_decode_attn")
     wb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     return _call(load().pkv_decode_attn_ex,
                  (ctypes.byref(c), _ptr(q), _CODE[q.dtype], B, Hq, _ptr(block_tables),
@@ -433,6 +454,8 @@ def pkv_decode_attn_noalloc(cache: KVCache, q: torch.Tensor, block_tables: torch
     callers that cannot allocate); see include/pkv.h for the size limit and sharing."""
     c = cache.struct()
     B, Hq, _ = q.shape
+    if cache.kv_dtype in BLOCK_SCALED:
+        _rows_out(cache, q, out, "pkv_decode_attn_noalloc")
     _check(load().pkv_decode_attn_noalloc_ex(ctypes.byref(c), _ptr(q), _CODE[q.dtype], B, Hq,
                                              _ptr(block_tables), int(block_tables.shape[1]),
                                              _ptr(context_lens), float(scale), _ptr(out),
@@ -469,6 +492,8 @@ def pkv_prefill_chunk_attn(cache: KVCache, q: torch.Tensor, q_start_loc: torch.T
     c = cache.struct()
     B = int(context_lens.shape[0])
     Hq = int(q.shape[1])
+    if cache.kv_dtype in BLOCK_SCALED:
+        _rows_out(cache, q, out, "pkv_prefill_chunk_attn")
     wb = 0 if workspace is None else workspace.numel() * workspace.element_size()
     return _call(load().pkv_prefill_chunk_attn_ex,
                  (ctypes.byref(c), _ptr(q), _CODE[q.dtype], B, Hq, _ptr(q_start_loc),

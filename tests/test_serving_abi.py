@@ -158,6 +158,30 @@ def test_binding_refuses_what_it_cannot_pass_on(lib):
         pkv.RopeParams(64, layout="other")
 
 
+@pytest.mark.parametrize("kv_dtype", [pkv.INT8B, pkv.FP8B])
+def test_binding_refuses_rows_that_are_not_dense(lib, kv_dtype):
+    cache = pkv.KVCache.allocate(4, 2, 64, kv_dtype, device="cpu")
+    slots = torch.zeros(3, dtype=torch.int32)
+    rows = torch.zeros(3, 2, 64)
+    for k, v in ((rows[:2], rows), (rows, torch.zeros(3, 4, 64)[:, ::2]), (rows, rows.bfloat16()),
+                 (torch.zeros(2, 3, 64).transpose(0, 1), rows), (torch.zeros(3, 2, 128), torch.zeros(3, 2, 128))):
+        with pytest.raises(ValueError, match="contiguous"):
+            pkv.pkv_append(cache, k, v, slots)
+    pkv.pkv_append(cache, rows, rows, slots, stream=0, bound=True)
+    bt, lens = torch.zeros(3, 1, dtype=torch.int32), torch.ones(3, dtype=torch.int32)
+    starts = torch.arange(4, dtype=torch.int32)
+    q = torch.zeros(3, 4, 64)
+    for x, out in ((torch.zeros(4, 3, 64).transpose(0, 1), q), (q, torch.zeros(3, 8, 64)[:, ::2]), (q, q.bfloat16()),
+                   (q, q[:2]), (torch.zeros(3, 4, 128), torch.zeros(3, 4, 128))):
+        with pytest.raises(ValueError, match="contiguous"):
+            pkv.pkv_decode_attn(cache, x, bt, lens, 0.125, out)
+        with pytest.raises(ValueError, match="contiguous"):
+            pkv.pkv_decode_attn_noalloc(cache, x, bt, lens, 0.125, out)
+        with pytest.raises(ValueError, match="contiguous"):
+            pkv.pkv_prefill_chunk_attn(cache, x, starts, 1, bt, lens, 0.125, out)
+    pkv.pkv_decode_attn(cache, q, bt, lens, 0.125, q.clone(), stream=0, bound=True)
+
+
 def test_bound_calls_are_not_issued(monkeypatch):
     calls = []
 
