@@ -174,7 +174,7 @@ __device__ __forceinline__ uint32_t block_recode4(uint32_t w, float by) {
 }
 
 template <bool FP8, int NEW_DT, int D>
-__global__ void __launch_bounds__(kBlockWarps * 32)
+__global__ void __launch_bounds__(kBlockWarps * 32, NEW_DT == kBF16 ? 5 : 1)
     append_block_kernel(uint8_t* __restrict__ k_cache, uint8_t* __restrict__ v_cache,
                         float* __restrict__ k_scale, float* __restrict__ v_scale,
                         const void* __restrict__ k_new, const void* __restrict__ v_new,
@@ -222,41 +222,54 @@ __global__ void __launch_bounds__(kBlockWarps * 32)
     for (int i = 0; i < E; ++i)
       was[i] = fetch ? reinterpret_cast<const uint4*>(block)[which ? lane * E + i : lane + 32 * i]
                      : make_uint4(0u, 0u, 0u, 0u);
-    float x[kPage][E];  // the token at page offset t, elements lane * E ..
-    float amax = 0.f;
+    // the token at page offset t, elements lane * E .. (BF16 pairs stay packed: 32 registers
+    // fewer at head_dim 128)
+    constexpr int W = NEW_DT == kBF16 ? E / 2 : E;
+    uint32_t raw[kPage][W];
 #pragma unroll
     for (int t = 0; t < kPage; ++t) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[t][e] = 0.f;
+      for (int e = 0; e < W; ++e) raw[t][e] = 0u;
       if (t >= off && t < off + n) {
         const size_t at = (static_cast<size_t>(tok + t - off) * Hkv + h) * D + lane * E;
-        if constexpr (NEW_DT == kBF16) {
-          uint32_t v[E / 2];
-          if constexpr (E == 4) {
-            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(src) + at);
-            v[0] = u.x;
-            v[E / 2 - 1] = u.y;
-          } else {
-            v[0] = *reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(src) + at);
-          }
-#pragma unroll
-          for (int e = 0; e < E; e += 2) {
-            x[t][e] = __uint_as_float(v[e / 2] << 16);
-            x[t][e + 1] = __uint_as_float(v[e / 2] & 0xffff0000u);
-          }
-        } else if constexpr (E == 4) {
-          const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(src) + at);
-          x[t][0] = v.x; x[t][1] = v.y; x[t][2] = v.z; x[t][3] = v.w;
+        const uint8_t* const p = static_cast<const uint8_t*>(src) + at * (NEW_DT == kBF16 ? 2 : 4);
+        if constexpr (W == 4) {
+          const uint4 v = *reinterpret_cast<const uint4*>(p);
+          raw[t][0] = v.x; raw[t][1] = v.y; raw[t][2] = v.z; raw[t][3] = v.w;
+        } else if constexpr (W == 2) {
+          const uint2 v = *reinterpret_cast<const uint2*>(p);
+          raw[t][0] = v.x; raw[t][1] = v.y;
         } else {
-          const float2 v = *reinterpret_cast<const float2*>(static_cast<const float*>(src) + at);
-          x[t][0] = v.x; x[t][1] = v.y;
+          raw[t][0] = *reinterpret_cast<const uint32_t*>(p);
         }
       }
     }
+    auto value = [&](int t, int e) -> float {
+      if constexpr (NEW_DT == kBF16) {
+        const uint32_t v = raw[t][e / 2];
+        return __uint_as_float(e & 1 ? v & 0xffff0000u : v << 16);
+      } else {
+        return __uint_as_float(raw[t][e]);
+      }
+    };
+    float amax = 0.f;
+    if constexpr (NEW_DT == kBF16) {
+      __nv_bfloat162 top = __float2bfloat162_rn(0.f);
 #pragma unroll
-    for (int t = 0; t < kPage; ++t)
+      for (int t = 0; t < kPage; ++t)
 #pragma unroll
-      for (int e = 0; e < E; ++e) amax = fmaxf(amax, fabsf(x[t][e]));
+        for (int e = 0; e < W; ++e) {
+          const uint32_t v = raw[t][e] & 0x7fff7fffu;
+          top = __hmax2(top, *reinterpret_cast<const __nv_bfloat162*>(&v));
+        }
+      const float2 f = __bfloat1622float2(top);
+      amax = fmaxf(f.x, f.y);
+    } else {
+#pragma unroll
+      for (int t = 0; t < kPage; ++t)
+#pragma unroll
+        for (int e = 0; e < E; ++e) amax = fmaxf(amax, fabsf(value(t, e)));
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const float need = block_scale<FP8>(amax);
@@ -281,7 +294,7 @@ __global__ void __launch_bounds__(kBlockWarps * 32)
       for (int t = 0; t < kPage; ++t) {
         if (t < off || t >= off + n) continue;
         uint8_t* const row = block + t * D + lane * E;
-        const uint32_t m = block_codes4<FP8>(x[t][0], x[t][1], x[t][E - 2], x[t][E - 1], s, inv);
+        const uint32_t m = block_codes4<FP8>(value(t, 0), value(t, 1), value(t, E - 2), value(t, E - 1), s, inv);
         if constexpr (E == 4) *reinterpret_cast<uint32_t*>(row) = m;
         else *reinterpret_cast<uint16_t*>(row) = static_cast<uint16_t>(m);
       }
@@ -303,7 +316,7 @@ __global__ void __launch_bounds__(kBlockWarps * 32)
           if (again && m_old[u]) w[u] = (w[u] & ~m_old[u]) | (block_recode4<FP8>(w[u], by) & m_old[u]);
           if (m_new[u])
             w[u] = (w[u] & ~m_new[u]) |
-                   (block_codes4<FP8>(x[4 * u][i], x[4 * u + 1][i], x[4 * u + 2][i], x[4 * u + 3][i], s, inv) &
+                   (block_codes4<FP8>(value(4 * u, i), value(4 * u + 1, i), value(4 * u + 2, i), value(4 * u + 3, i), s, inv) &
                     m_new[u]);
         }
         reinterpret_cast<uint4*>(block)[lane * E + i] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -316,10 +329,13 @@ template <bool FP8>
 cudaError_t launch_block(const CacheView& c, void* k, void* v, float* ks, float* vs, const void* kn,
                          const void* vn, int new_dtype, const int32_t* slots, int T,
                          int32_t* dev_status, cudaStream_t st) {
-  // Tokens per warp: one while every token can have its own warps at once (a decode step's
-  // tokens each lie in a page of their own), else 8 (a prompt's tokens share pages: with
-  // one token per warp, 15 of 16 warps only find that they do not lead a run).
-  const int group = 2ll * T * c.Hkv <= 152 * 16 ? 1 : 8;
+  // Tokens per warp: as few as keep the launch to about 32 warps an SM, all resident at once
+  // (a decode step's tokens each lie in a page of their own and have their own warps; a
+  // prompt's tokens share pages, and with one token per warp 15 of 16 only find that they do
+  // not lead a run).  BF16 rows, 2 heads of 128, us at 1 / 4 / 8 / 16 tokens a warp: 4.6k tokens
+  // 16.6 / 5.2 / 5.9 / 7.0, 16k tokens 54 / 23.2 / 20.1 / 17.9.
+  int group = 1;
+  while (group < 16 && 2ll * ((T + group - 1) / group) * c.Hkv > 152 * 32) group *= group == 1 ? 4 : 2;
   const long long items = 2ll * ((T + group - 1) / group) * c.Hkv;
   if (items / kBlockWarps >= 0x7fffffffll) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>((items + kBlockWarps - 1) / kBlockWarps));
