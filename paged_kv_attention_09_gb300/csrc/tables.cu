@@ -35,6 +35,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPer = 4;                       // requests per thread of a chunk
 constexpr int kChunk = kThreads * kPer;       // requests per chunk
+// (A step of 32k rows: 11.5 us at 256, 10.9 at 1024, 12.9 at 2048.)
 constexpr int kRowsPerBlock = 1024;
 constexpr int kBackRounds = 8;  // returned pages per thread and round
 constexpr int kMaxBlocks = 1024;  // more rows than 1024 per block are taken in strides
