@@ -35,6 +35,10 @@
 //             (rows 0-7 / 8-15); per-token K scales multiply the scores and V scales the
 //             probabilities (split hi/lo) in FP32.  (The s8 MMA path is far slower on
 //             this part.)
+//             INT8B and FP8B (one scale for a page's 16 tokens, the layouts of INT8 and FP8)
+//             take it too, with one K and one V scale a page in place of the scale vectors;
+//             their INT8 codes lose the bias before the MMA (1152 + code - 1152, exact), as
+//             a score's error may not grow with a constant times the sum of the query.
 // The order of every floating-point reduction depends only on logical token positions,
 // the split size and the warp count, so results are bit-identical under any physical
 // page permutation.

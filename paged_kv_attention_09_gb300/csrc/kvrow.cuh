@@ -86,17 +86,6 @@ __device__ __forceinline__ float block_scale(float amax) {
     return __uint_as_float(static_cast<uint32_t>(e < 1 ? 1 : e) << 23);
   }
 }
-// The stored byte of x at scale s (0 when the block is all zero).
-template <bool FP8>
-__device__ __forceinline__ uint32_t block_code(float x, float s) {
-  if constexpr (!FP8) {
-    float r = 0.f;
-    if (s != 0.f) r = fminf(fmaxf(rintf(__fdiv_rn(x, s)), -127.f), 127.f);
-    return static_cast<uint32_t>(static_cast<int>(r) + 128);
-  } else {
-    return s != 0.f ? __nv_cvt_float_to_fp8(__fdiv_rn(x, s), __NV_SATFINITE, __NV_E4M3) : 0u;
-  }
-}
 // A stored byte coded again at a scale 1 / by times as large (by = old scale / new, < 1).
 template <bool FP8>
 __device__ __forceinline__ uint32_t block_recode(uint32_t byte, float by) {

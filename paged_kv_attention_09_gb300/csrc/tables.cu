@@ -12,13 +12,16 @@
 // keeps the chunk's offsets in shared memory; its own 1024 rows then find their request by
 // binary search there.  So no block waits for another, whatever the batch, and a single
 // long prompt spreads over as many blocks as a thousand short ones.  The first row of a new
-// page writes the table entry.  The last block also pushes the ended
-// requests' pages: behind the free ones, so that the places written are never those that
-// other blocks read new pages from.  The block that takes the last ticket (an atomic, no
-// waiting: every block has read the pool's state by then) updates the state, so that a step
-// works on the pool in place and can be replayed from a CUDA graph.
+// page writes the table entry.  The last block also pushes the ended requests' pages: behind
+// the free ones, so that the places written are never those that other blocks read new pages
+// from.  The block that takes the last ticket (an atomic, no waiting: every block has read the
+// pool's state by then) updates the state, so that a step works on the pool in place and can
+// be replayed from a CUDA graph.
 //
-// Bound by latency, not bytes: a 256-request decode step moves 9 KB.
+// Bound by latency, not bytes: a 256-request decode step moves 9 KB in 6.1 us (an empty launch
+// takes about 2, the rest is four dependent round trips: lengths, pages or table entries, the
+// ticket, the state).  A step of 511 requests with 32k prompt rows and ended requests takes
+// 10.9 us, 14 with the ended requests' pages behind the other blocks' rows in one block.
 #include <cuda_runtime.h>
 
 #include <cstdint>
