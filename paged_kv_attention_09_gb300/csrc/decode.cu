@@ -9,7 +9,7 @@
 //
 // Thread-block layout: grid (split, sequence, kv-head x head-group).  A block owns up to
 // 8 query heads that share one kv head, and a contiguous range of the sequence's
-// logical pages.  Each of its 4 warps streams every 4th page of that range
+// logical pages.  Each of its 4 (or 8) warps streams every 4th (8th) page of that range
 // through its own ring of shared-memory stages filled by 1-D bulk copies (TMA engine,
 // one copy per K block, V block and scale vector of a (page, kv-head)).  The producer
 // lane validates every page id just before issuing its copies, so the first copies are
@@ -120,15 +120,21 @@ struct RowBytes {
 #ifndef PKV_F32_STAGES
 #define PKV_F32_STAGES 2
 #endif
-template <int KVT, int D>
+template <int KVT, int D, bool WIDE = false>
 struct Tune {
   static constexpr int S = quantised(KVT) ? PKV_INT8_STAGES
                          : KVT == kBF16 ? (D == 64 ? 3 : PKV_BF16_STAGES)
                                         : (D == 64 ? PKV_F32_STAGES : 2);
   // Warps per block.  (Three-warp INT8 blocks, which leave 96 registers at 7 blocks per
   // SM, measured slower than four warps at 72 registers.)
-  static constexpr int W = 4;
-  static constexpr int minBlocks = (quantised(KVT) && D == 64) ? 7 : (KVT == kBF16 && D == 128) ? 3 : 1;
+  // Block-scaled formats: also wide blocks of 8 warps, for launches of at most one wave
+  // (plan_decode): as many warps a context in half the blocks, so half the partials to merge.
+  static constexpr int W = WIDE ? 8 : 4;
+  // (Block-scaled, head_dim 128: 256 x 1k takes 34.8 us at the 3 blocks that 140 registers
+  // allow, 23.9 at 4.)
+  static constexpr int minBlocks = WIDE ? (D == 128 ? 2 : 3)
+                                 : block_scaled(KVT) && D == 128 ? 4
+                                 : (quantised(KVT) && D == 64) ? 7 : (KVT == kBF16 && D == 128) ? 3 : 1;
 };
 
 template <int KVT, int D>
@@ -142,11 +148,11 @@ struct Layout {
   static constexpr int stageBytes = pageBytes;
 };
 
-template <int KVT, int D, bool STEP = false>
+template <int KVT, int D, bool STEP = false, bool WIDE = false>
 struct Smem {
   using Lo = Layout<KVT, D>;
-  static constexpr int kW = Tune<KVT, D>::W;
-  static constexpr int stages = kW * Lo::S * Lo::stageBytes;
+  static constexpr int kW = Tune<KVT, D, WIDE>::W;
+  static constexpr int stages = kW * Tune<KVT, D, WIDE>::S * Lo::stageBytes;
   // merge area: per-warp max[8], sum[8], acc[8][D+2], then weights [warp][8] (floats)
   // (+ the block's partial for the on-chip split merge: max[8], sum[8], O[8][D])
   static constexpr int combine =
@@ -1090,13 +1096,13 @@ __device__ __noinline__ void cluster_merge(const DParams& p, const float* part, 
 
 // WIN: compiled with the sliding-window range and mask (the kernels without it carry no
 // trace of it: the INT8 kernel sits at its register budget)
-template <int KVT, int D, bool STEP, bool WIN>
-__global__ void __launch_bounds__(Tune<KVT, D>::W * 32, Tune<KVT, D>::minBlocks)
+template <int KVT, int D, bool STEP, bool WIN, bool WIDE>
+__global__ void __launch_bounds__(Tune<KVT, D, WIDE>::W * 32, Tune<KVT, D, WIDE>::minBlocks)
     decode_kernel(const __grid_constant__ DParams p) {
   using Lo = Layout<KVT, D>;
-  using Sm = Smem<KVT, D, STEP>;
+  using Sm = Smem<KVT, D, STEP, WIDE>;
   constexpr int S = Lo::S;
-  constexpr int kW = Tune<KVT, D>::W, kThreads = kW * 32;
+  constexpr int kW = Tune<KVT, D, WIDE>::W, kThreads = kW * 32;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* stages = smem;
   float* probs_all = reinterpret_cast<float*>(smem + Sm::big);
@@ -1675,7 +1681,10 @@ __global__ void __launch_bounds__(Tune<KVT, D>::W * 32, Tune<KVT, D>::minBlocks)
     const size_t row0 = static_cast<size_t>(b) * p.Hq + h0;
     constexpr int D4 = D / 4;
     constexpr int CPT = (kMaxHeads * D4 + kThreads - 1) / kThreads;  // chunks per thread
-    constexpr int SB = 8;                                             // splits per batch
+    // thread groups that share the splits (group j takes j, j + NG, ...), splits per batch
+    constexpr int NG = kThreads > kMaxHeads * D4 ? kThreads / (kMaxHeads * D4) : 1;
+    constexpr int SB = WIDE && D == 128 ? 16 : 8;
+    const int grp = NG > 1 ? tid / (kMaxHeads * D4) : 0;
     const size_t sstride = stride * D4;  // float4s from one split's partial to the next
     const float4* src[CPT];
     int rr[CPT];
@@ -1686,7 +1695,7 @@ __global__ void __launch_bounds__(Tune<KVT, D>::W * 32, Tune<KVT, D>::minBlocks)
     constexpr bool kEarly = !(quantised(KVT) && D == 64);
 #pragma unroll
     for (int c = 0; c < CPT; ++c) {
-      const int cidx = tid + c * kThreads;
+      const int cidx = tid - grp * (kMaxHeads * D4) + c * kThreads;
       act[c] = cidx < nh * D4;
       rr[c] = act[c] ? cidx / D4 : 0;
       src[c] = reinterpret_cast<const float4*>(p.ws_o + (row0 + rr[c]) * D) + (act[c] ? cidx % D4 : 0);
@@ -1694,7 +1703,8 @@ __global__ void __launch_bounds__(Tune<KVT, D>::W * 32, Tune<KVT, D>::minBlocks)
       if constexpr (kEarly) {
 #pragma unroll
         for (int k = 0; k < SB; ++k)
-          v[c][k] = act[c] && k < nsplit ? __ldcg(src[c] + k * sstride) : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[c][k] = act[c] && k * NG + grp < nsplit ? __ldcg(src[c] + (k * NG + grp) * sstride)
+                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
       }
     }
     __syncthreads();
@@ -1724,27 +1734,39 @@ __global__ void __launch_bounds__(Tune<KVT, D>::W * 32, Tune<KVT, D>::minBlocks)
       if (lane == 0) wts[nsplit * kMaxHeads + r] = poisoned ? CUDART_NAN_F : (Ls > 0.f ? 1.f / Ls : 0.f);
     }
     __syncthreads();
-    for (int s0 = 0; s0 < nsplit; s0 += SB) {
-      if (s0 > 0 || !kEarly) {
+    for (int s0 = grp; s0 < nsplit; s0 += SB * NG) {
+      if (s0 > grp || !kEarly) {
 #pragma unroll
         for (int c = 0; c < CPT; ++c)
 #pragma unroll
           for (int k = 0; k < SB; ++k)
-            v[c][k] = act[c] && s0 + k < nsplit ? __ldcg(src[c] + (s0 + k) * sstride)
-                                                : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[c][k] = act[c] && s0 + k * NG < nsplit ? __ldcg(src[c] + (s0 + k * NG) * sstride)
+                                                     : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
       for (int c = 0; c < CPT; ++c)
 #pragma unroll
         for (int k = 0; k < SB; ++k) {
-          if (s0 + k < nsplit) {
-            const float wt = wts[(s0 + k) * kMaxHeads + rr[c]];
+          if (s0 + k * NG < nsplit) {
+            const float wt = wts[(s0 + k * NG) * kMaxHeads + rr[c]];
             acc[c].x += v[c][k].x * wt;
             acc[c].y += v[c][k].y * wt;
             acc[c].z += v[c][k].z * wt;
             acc[c].w += v[c][k].w * wt;
           }
         }
+    }
+    if constexpr (NG > 1) {  // the groups' sums, in the groups' order
+      float4* const sums = reinterpret_cast<float4*>(lsm + nsplit * kMaxHeads);
+      if (grp > 0) sums[tid - kMaxHeads * D4] = acc[0];
+      __syncthreads();
+      act[0] = act[0] && grp == 0;
+#pragma unroll
+      for (int j = 1; j < NG; ++j) {
+        if (!act[0]) break;
+        const float4 x = sums[tid + (j - 1) * kMaxHeads * D4];
+        acc[0].x += x.x; acc[0].y += x.y; acc[0].z += x.z; acc[0].w += x.w;
+      }
     }
 #pragma unroll
     for (int c = 0; c < CPT; ++c) {
@@ -1761,9 +1783,9 @@ __global__ void __launch_bounds__(Tune<KVT, D>::W * 32, Tune<KVT, D>::minBlocks)
   if (tid == 0) *ticket = 0;  // leave the counter ready for the next call
 }
 
-template <int KVT, int D, bool STEP, bool WIN>
+template <int KVT, int D, bool STEP, bool WIN, bool WIDE = false>
 const void* kernel_ptr() {
-  return reinterpret_cast<const void*>(&decode_kernel<KVT, D, STEP, WIN>);
+  return reinterpret_cast<const void*>(&decode_kernel<KVT, D, STEP, WIN, WIDE>);
 }
 
 struct Variant {
@@ -1774,9 +1796,10 @@ struct Variant {
   int warps;       // warps per block
 };
 
-template <int KVT, int D>
+template <int KVT, int D, bool WIDE = false>
 constexpr int max_splits_of() {
-  return Smem<KVT, D>::big / (2 * kMaxHeads * 4) - 1;
+  constexpr int groups = Tune<KVT, D, WIDE>::W * 32 / (kMaxHeads * D / 4);  // (their sums, too)
+  return (Smem<KVT, D, false, WIDE>::big - (groups > 1 ? (groups - 1) * kMaxHeads * D * 4 : 0)) / (2 * kMaxHeads * 4) - 1;
 }
 
 #define PKV_VARIANT(T, D, ST, WN, I)                                                        \
@@ -1784,9 +1807,9 @@ constexpr int max_splits_of() {
    Tune<T, D>::W}
 // index: dtype-and-head-dim slot (0 .. 9), + 10 for the fused decode step, + 20 for the
 // sliding window; 40 .. 47 the block-scaled formats (no fused step: a new row can change
-// its whole block's codes)
-constexpr int kVariants = 48;
-Variant variant(int dtype, int D, bool step, bool win) {
+// its whole block's codes), 48 .. 55 their wide blocks
+constexpr int kVariants = 56;
+Variant variant(int dtype, int D, bool step, bool win, bool wide) {
   switch (dtype * 1000 + D + (step ? 100000 : 0) + (win ? 1000000 : 0)) {
 #define PKV_VARIANTS_OF(ST, WN, BASE, KEY)                                                \
     case KEY + kF32 * 1000 + 64: return PKV_VARIANT(kF32, 64, ST, WN, BASE + 0);          \
@@ -1804,14 +1827,22 @@ Variant variant(int dtype, int D, bool step, bool win) {
     PKV_VARIANTS_OF(false, true, 20, 1000000)
     PKV_VARIANTS_OF(true, true, 30, 1100000)
 #undef PKV_VARIANTS_OF
-#define PKV_VARIANTS_OF(WN, BASE, KEY)                                                    \
-    case KEY + kINT8B * 1000 + 64: return PKV_VARIANT(kINT8B, 64, false, WN, BASE + 0);   \
-    case KEY + kINT8B * 1000 + 128: return PKV_VARIANT(kINT8B, 128, false, WN, BASE + 1); \
-    case KEY + kFP8B * 1000 + 64: return PKV_VARIANT(kFP8B, 64, false, WN, BASE + 2);     \
-    case KEY + kFP8B * 1000 + 128: return PKV_VARIANT(kFP8B, 128, false, WN, BASE + 3);
-    PKV_VARIANTS_OF(false, 40, 0)
-    PKV_VARIANTS_OF(true, 44, 1000000)
+#define PKV_BLOCK_VARIANT(T, D, WN, WD, I)                                                  \
+  {kernel_ptr<T, D, false, WN, WD>(), Smem<T, D, false, WD>::total, I, max_splits_of<T, D, WD>(), Tune<T, D, WD>::W}
+#define PKV_VARIANTS_OF(T, D, KEY, I)                                                     \
+    case KEY + T * 1000 + D:                                                              \
+      if (wide) return PKV_BLOCK_VARIANT(T, D, KEY != 0, true, I + 8);                    \
+      return PKV_BLOCK_VARIANT(T, D, KEY != 0, false, I);
+    PKV_VARIANTS_OF(kINT8B, 64, 0, 40)
+    PKV_VARIANTS_OF(kINT8B, 128, 0, 41)
+    PKV_VARIANTS_OF(kFP8B, 64, 0, 42)
+    PKV_VARIANTS_OF(kFP8B, 128, 0, 43)
+    PKV_VARIANTS_OF(kINT8B, 64, 1000000, 44)
+    PKV_VARIANTS_OF(kINT8B, 128, 1000000, 45)
+    PKV_VARIANTS_OF(kFP8B, 64, 1000000, 46)
+    PKV_VARIANTS_OF(kFP8B, 128, 1000000, 47)
 #undef PKV_VARIANTS_OF
+#undef PKV_BLOCK_VARIANT
     default: return {nullptr, 0, -1, 1, 4};
   }
 }
@@ -1888,7 +1919,7 @@ int clusters_resident(int device, const Variant& v, int n) {
 bool plan_decode(const CacheView& c, int B, int Hq, int MB, int q_dtype, int device,
                  int chunk_override, DecodePlan* plan, bool step) {
   (void)q_dtype;
-  const Variant v = variant(c.dtype, c.D, step, c.window > 0);
+  Variant v = variant(c.dtype, c.D, step, c.window > 0, false);
   if (!v.fn) return false;
   const int G = Hq / c.Hkv;
   const int cap = (c.dtype == kF32 && c.D == 128) ? f32_head_cap<128>() : kMaxHeads;
@@ -1903,6 +1934,23 @@ bool plan_decode(const CacheView& c, int B, int Hq, int MB, int q_dtype, int dev
   }
   int sms = 0, occ = 0;
   if (!device_facts(device, v, &sms, &occ)) return false;
+  const long long units = static_cast<long long>(B) * c.Hkv * plan->head_groups;
+  // Block-scaled formats: wide blocks while the units fit in one wave of them.  (us, narrow
+  // and wide: 4 ragged contexts of 32k, heads of 128, 18.9 and 16.8; 32 x 2k 13.2 and 12.4;
+  // 128 x 1k 16.1 and 13.9; heads of 64: 1 x 32k 19.0 and 14.9, 96 x 1k 17.5 and 13.5, 2 x 1k 8.4
+  // and 7.8.  Over one wave: 160 x 1k, heads of 64, 17.6 and 18.9; 200 x 1k, heads of 128, 18.4
+  // and 21.5.)
+  plan->wide = 0;
+  if (block_scaled(c.dtype)) {
+    const Variant wv = variant(c.dtype, c.D, step, c.window > 0, true);
+    int wocc = 0;
+    if (!device_facts(device, wv, &sms, &wocc)) return false;
+    if (units <= static_cast<long long>(sms) * wocc) {
+      plan->wide = 1;
+      v = wv;
+      occ = wocc;
+    }
+  }
   int chunk;
   if (chunk_override > 0) {
     chunk = chunk_override;
@@ -1911,17 +1959,14 @@ bool plan_decode(const CacheView& c, int B, int Hq, int MB, int q_dtype, int dev
     // do not split: merges cost more than the last partial wave.  Otherwise aim for
     // about two blocks per slot at full table length, with at least 8 pages per warp and
     // at most 32 splits, so that the partial merge stays short.
-    const long long units = static_cast<long long>(B) * c.Hkv * plan->head_groups;
     const long long slots = static_cast<long long>(sms) * occ;
     long long splits = 1;
     if (units > 0 && 4 * units < 3 * slots && block_scaled(c.dtype)) {
       // Block-scaled formats (added later, so the others' plans and sums stay as they are):
-      // as many splits as fill the slots once at full table length, with at least 4 pages
-      // per warp and at most 64 splits.  (us, by this rule and by the one below: 4 ragged
-      // contexts of 32k, heads of 128, 19.1 and 21.0; 32 x 2k 13.2 and 13.9; 8 x 4k 12.5 and
-      // 14.8; 2 x 1k, heads of 64, 8.3 and 10.2.)
+      // as many splits as fill the slots once at full table length, with at least 2 pages
+      // per warp (8 x 4k, heads of 128: 11.0 us, 13.0 with 4) and at most 64 splits.
       splits = slots / units;
-      const long long by_len = mb / (4 * v.warps);
+      const long long by_len = mb / (2 * v.warps);
       if (splits > by_len) splits = by_len;
       if (splits > 64) splits = 64;
       if (splits < 1) splits = 1;
@@ -1957,7 +2002,7 @@ bool plan_decode(const CacheView& c, int B, int Hq, int MB, int q_dtype, int dev
 }
 
 cudaError_t launch_decode(const DecodeArgs& a, const DecodePlan& plan, cudaStream_t st) {
-  const Variant v = variant(a.c.dtype, a.c.D, a.step, a.c.window > 0);
+  const Variant v = variant(a.c.dtype, a.c.D, a.step, a.c.window > 0, plan.wide);
   if (!v.fn) return cudaErrorInvalidValue;
   DParams p{};
   p.k = static_cast<const uint8_t*>(a.c.k);

@@ -50,6 +50,7 @@ struct DecodePlan {
   int chunk_pages;    // pages per thread block
   int n_splits;       // grid.x = ceil(max_blocks / chunk_pages)
   int cluster;        // 1: the n_splits blocks of a sequence form a cluster and merge on chip
+  int wide;           // 1: blocks of more warps (block-scaled caches)
   size_t ws_bytes;    // workspace bytes (0 for on-chip merges)
 };
 
