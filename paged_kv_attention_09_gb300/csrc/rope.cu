@@ -24,9 +24,9 @@
 // thread walks over, and partly turned heads cost nothing extra.  Rows, strides or sizes
 // that are not multiples of 16 bytes take a plain element-by-element kernel.
 // Bound by HBM: every element is read once and written once.  65536 tokens of 36 BF16 heads of
-// 64: 93 us, 6.5 TB/s; 8192 tokens of 14 heads of 128 out of fused rows: 12.6 us, 4.7 TB/s (one
-// wave of blocks: half the time is the launch's ramp and the last block's round trip); a decode
-// step of 256 tokens is bound by latency, 2.5 us.
+// 64: 91 us, 6.6 TB/s; 8192 tokens of 14 heads of 128 out of fused rows: 11.7 us, 5.0 TB/s (one
+// wave of blocks: the launch's ramp and the last blocks' round trips are the rest); a decode
+// step of 64 tokens is bound by latency, 2.5 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -146,37 +146,41 @@ __global__ void __launch_bounds__(kThreads) rope_rows_kernel(const __grid_consta
     if (a.status) atomicOr(a.status, 0x10);  // PKV_DEV_TIMEOUT
     return;
   }
-  const int per_token = H * units;
+  // A thread keeps the angles of VE pairs of a token and turns every `share`-th head by them (the
+  // prefill above: 12.5 us with the angles read again for each head).
+  const int share = max(1, min(H, kThreads / (nt * units))), per_token = share * units;
   for (int i = tid; i < nt * per_token; i += kThreads) {
-    const int t = i / per_token, r = i - t * per_token, h = r / units, j = r - h * units;
-    uint8_t* const px = smem + t * row + (h * D + (HALF ? j * VE : 2 * j * VE)) * sizeof(T);
-    uint8_t* const py = px + (HALF ? half : VE) * sizeof(T);
+    const int t = i / per_token, it = i - t * per_token, h0 = it / units, j = it - h0 * units;
     float c[VE], s[VE];
 #pragma unroll
     for (int e = 0; e < VE; e += 2) {
       const float4 v = *reinterpret_cast<const float4*>(angles + 2 * (t * half + (e / 2 * units + j) * 2));
       c[e] = v.x; s[e] = v.y; c[e + 1] = v.z; s[e + 1] = v.w;
     }
-    float x[VE], y[VE], u[VE], v[VE];
-    widen<T, VE>(*reinterpret_cast<const uint4*>(px), x);
-    widen<T, VE>(*reinterpret_cast<const uint4*>(py), y);
-    if constexpr (HALF) {
+    uint8_t* px = smem + t * row + (h0 * D + (HALF ? j * VE : 2 * j * VE)) * sizeof(T);
+    for (int h = h0; h < H; h += share, px += share * D * sizeof(T)) {
+      uint8_t* const py = px + (HALF ? half : VE) * sizeof(T);
+      float x[VE], y[VE], u[VE], v[VE];
+      widen<T, VE>(*reinterpret_cast<const uint4*>(px), x);
+      widen<T, VE>(*reinterpret_cast<const uint4*>(py), y);
+      if constexpr (HALF) {
 #pragma unroll
-      for (int e = 0; e < VE; ++e) {
-        u[e] = fmaf(x[e], c[e], -(y[e] * s[e]));
-        v[e] = fmaf(y[e], c[e], x[e] * s[e]);
-      }
-    } else {  // pairs lie side by side: VE / 2 of them in each vector
+        for (int e = 0; e < VE; ++e) {
+          u[e] = fmaf(x[e], c[e], -(y[e] * s[e]));
+          v[e] = fmaf(y[e], c[e], x[e] * s[e]);
+        }
+      } else {  // pairs lie side by side: VE / 2 of them in each vector
 #pragma unroll
-      for (int e = 0; e < VE / 2; ++e) {
-        u[2 * e] = fmaf(x[2 * e], c[e], -(x[2 * e + 1] * s[e]));
-        u[2 * e + 1] = fmaf(x[2 * e + 1], c[e], x[2 * e] * s[e]);
-        v[2 * e] = fmaf(y[2 * e], c[VE / 2 + e], -(y[2 * e + 1] * s[VE / 2 + e]));
-        v[2 * e + 1] = fmaf(y[2 * e + 1], c[VE / 2 + e], y[2 * e] * s[VE / 2 + e]);
+        for (int e = 0; e < VE / 2; ++e) {
+          u[2 * e] = fmaf(x[2 * e], c[e], -(x[2 * e + 1] * s[e]));
+          u[2 * e + 1] = fmaf(x[2 * e + 1], c[e], x[2 * e] * s[e]);
+          v[2 * e] = fmaf(y[2 * e], c[VE / 2 + e], -(y[2 * e + 1] * s[VE / 2 + e]));
+          v[2 * e + 1] = fmaf(y[2 * e + 1], c[VE / 2 + e], y[2 * e] * s[VE / 2 + e]);
+        }
       }
+      *reinterpret_cast<uint4*>(px) = narrow<T, VE>(u);
+      *reinterpret_cast<uint4*>(py) = narrow<T, VE>(v);
     }
-    *reinterpret_cast<uint4*>(px) = narrow<T, VE>(u);
-    *reinterpret_cast<uint4*>(py) = narrow<T, VE>(v);
   }
   fence_proxy_async_smem();  // the turned rows are visible to the copies
   __syncthreads();
