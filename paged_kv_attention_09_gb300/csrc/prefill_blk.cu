@@ -35,7 +35,7 @@
 // take 1600 and the fills less.  Measured (cycles a tile; 4 x 512 tokens over 4096, 12 / 2 heads
 // of 128, FP8B): 4400 with the codes through registers or asynchronous copies and one MMA
 // issuer, 3300 with whole runs of 64 keys per warp and no bank conflicts, 2600 with two issuers.
-// That workload: 55.0 us, 618 TFLOP/s; 2 chunks of 512 over 2048: 35.1 us.
+// That workload: 54.3 us, 627 TFLOP/s; 2 chunks of 512 over 2048: 34.7 us; one chunk of 37: 8.7 us.
 //
 // Range of FP16: query rows are brought to [2^13, 2^14) by a power of two that goes into the
 // score scale (float queries as high part + remainder); probabilities carry the V scale as
@@ -205,6 +205,13 @@ __global__ void __launch_bounds__(BSmem<D, QSPLIT>::threads, 1)
   const int g = blockIdx.y, b = blockIdx.z;
   const int tile = blockIdx.x / p.ksplit, ks = blockIdx.x % p.ksplit;
   const int row0 = tile * kRowsTC;
+  // the warps that fetch codes: their place among K's or V's, and the first page ids, read
+  // together with the lengths where the range's first page does not depend on those
+  const bool fills = warp >= kKWarp, isK = warp < kVWarp;
+  const int step = isK ? kKWarps : Sm::VW, w = warp - (isK ? kKWarp : kVWarp);
+  const int q_first = kPagesTC * w + (lane & 3);
+  const bool early = p.window == 0 && ks == 0;
+  int ids = fills && early && q_first < p.MB ? p.bt[static_cast<size_t>(b) * p.MB + q_first] : -1;
   const int q0 = p.qsl[b];
   const int Lq = p.qsl[b + 1] - q0;
   const int L = p.lens[b];
@@ -234,20 +241,88 @@ __global__ void __launch_bounds__(BSmem<D, QSPLIT>::threads, 1)
   const int n_tiles = t1 - t0;
   const int32_t* btw = p.bt + static_cast<size_t>(b) * p.MB + kbase / kPage;
 
+  // ---- what a block's start waits for goes out before it is set up: the first codes and the
+  // query rows.  A page id outside the pool is replaced by page 0 (every read stays inside the
+  // cache) and flagged: the block's rows then become NaN.
+  bool bad = false;
+  auto checked = [&](int q, int id) -> int {  // -1: no such page
+    if (q >= n_pages) return -1;
+    if (id >= 0 && id < p.num_pages) return id;
+    bad = true;
+    return 0;
+  };
+  auto page_id = [&](int q) -> int { return checked(q, q < n_pages ? btw[q] : -1); };
+  const int n_halves = 2 * n_tiles;
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t slot = sbase + (isK ? Sm::rk0 : Sm::rv0) + w * Sm::raw;
+  const uint32_t bar = smem_u32(&bars[Sm::rawFull + warp - kKWarp]);
+  auto request = [&](int h) {  // the copies of run h, h = w, w + step, ...
+    if (h < n_halves) {
+      const int n = min(kPagesTC, max(0, n_pages - kPagesTC * h));  // its pages
+      mbar_arrive_expect_tx_if(lane == 0, bar, n * Sm::page);
+      const bool there = lane < n;
+      const size_t blk = there ? static_cast<size_t>(ids) * p.Hkv + g : 0;
+      __syncwarp();
+      bulk_g2s_if(there, slot + lane * Sm::page, (isK ? p.k : p.v) + blk * Sm::page, Sm::page, bar,
+                  l2_evict_last_policy());  // every row tile of the group rereads them
+      if (isK && lane < kPagesTC) {
+        const uint32_t at = sbase + Sm::sc0 + (h >> 1) % kScaleSlots * Sm::scSlot + ((h & 1) * kPagesTC + lane) * 4;
+        if (there) {
+          fetch4(at, p.ks + blk);
+          fetch4(at + 4 * kPagesB, p.vs + blk);
+        } else {  // no page: zeros (its keys are masked)
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(0) : "memory");
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 4 * kPagesB), "r"(0) : "memory");
+        }
+      }
+      // the ids of the warp's next 64 keys (lanes 0 .. 3), loaded one run ahead: read when
+      // needed they would cost a global round trip
+      ids = page_id(kPagesTC * (h + step) + (lane & 3));
+    }
+    fetch_commit();
+  };
+  // softmax threads: row r (= TMEM lane 32 (warp % 4) + lane), part of the row
+  const int r = tid & (kRowsTC - 1);
+  const int part = tid / kRowsTC;
+  const int rho = row0 + r;
+  const bool valid_row = tid < kSoftThreads && rho < nrows;
+  constexpr int N = D / kParts;                       // its columns of the query row
+  constexpr int QN = QSPLIT ? N / 4 : N / 8;          // in 16-byte pieces
+  uint4 qraw[QN];
+#pragma unroll
+  for (int i = 0; i < QN; ++i) qraw[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (n_tiles > 0) {
+    if (fills) {
+      if (lane == 0) {
+        mbar_init(&bars[Sm::rawFull + warp - kKWarp], 1);
+        fence_barrier_init();
+      }
+      __syncwarp();
+      ids = checked(q_first, early || q_first >= n_pages ? ids : btw[q_first]);
+      request(w);
+    } else if (valid_row) {
+      const size_t at = (static_cast<size_t>(q0 + rho / p.G) * p.Hq + g * p.G + rho % p.G) * D + N * part;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.q) + at * (QSPLIT ? 4 : 2));
+#pragma unroll
+      for (int i = 0; i < QN; ++i) qraw[i] = src[i];
+    }
+  }
+
   // ---- set-up: TMEM and barriers
   if (warp == kMmaWarp) {
     tc::tmem_alloc(tmem_slot, Sm::tmemCols);
     tc::tmem_relinquish();
   }
-  if (tid == 0) {
-    for (int i = 0; i < Sm::nbars; ++i) {
-      const int count = i >= Sm::kFull && i < Sm::kFull + Sm::KST     ? 2   // its halves
-                        : (i >= Sm::pFull && i < Sm::pFull + Sm::SB) || i == Sm::qFull ? kSoftWarps
-                        : i == Sm::fin                                ? 2  // one from each MMA issuer
-                                                                      : 1;
-      mbar_init(&bars[i], count);
-    }
+  if (tid < Sm::rawFull) {
+    const int i = tid;
+    const int count = i >= Sm::kFull && i < Sm::kFull + Sm::KST     ? 2   // its halves
+                      : (i >= Sm::pFull && i < Sm::pFull + Sm::SB) || i == Sm::qFull ? kSoftWarps
+                      : i == Sm::fin                                ? 2  // one from each MMA issuer
+                                                                    : 1;
+    mbar_init(&bars[i], count);
     fence_barrier_init();
+  }
+  if (tid == 0) {
     *abort_flag = 0;
     for (int i = 0; i < 4; ++i) soft_fail[i] = 0;
     s_err = err;
@@ -256,62 +331,12 @@ __global__ void __launch_bounds__(BSmem<D, QSPLIT>::threads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t sbase = smem_u32(smem);
 
-  // softmax threads: row r (= TMEM lane 32 (warp % 4) + lane), part of the row
-  const int r = tid & (kRowsTC - 1);
-  const int part = tid / kRowsTC;
-  const int rho = row0 + r;
-  const bool valid_row = tid < kSoftThreads && rho < nrows;
   const int quarter = warp & 3;
 
-  // A page id outside the pool is replaced by page 0 (every read stays inside the cache)
-  // and flagged: the block's rows then become NaN.
-  bool bad = false;
-  auto page_id = [&](int q) -> int {  // -1: no such page
-    if (q >= n_pages) return -1;
-    const int id = btw[q];
-    if (id >= 0 && id < p.num_pages) return id;
-    bad = true;
-    return 0;
-  };
-
   constexpr int UPP = D / 32;  // units of 32 pieces of 16 codes per page
-  const int n_halves = 2 * n_tiles;
-  if (n_tiles > 0 && warp >= kKWarp) {
+  if (n_tiles > 0 && fills) {
     // ---------------------------------------------------------------- K and V codes
-    const bool isK = warp < kVWarp;
-    const int step = isK ? kKWarps : Sm::VW, w = warp - (isK ? kKWarp : kVWarp);
-    const uint32_t slot = sbase + (isK ? Sm::rk0 : Sm::rv0) + w * Sm::raw;
-    const uint32_t bar = smem_u32(&bars[Sm::rawFull + warp - kKWarp]);
-    const uint64_t pol = l2_evict_last_policy();  // every row tile of the group rereads them
-    const uint8_t* const src = isK ? p.k : p.v;
-    // the ids of the warp's next 64 keys (lanes 0 .. 3), loaded one run ahead: read when
-    // needed they would cost a global round trip
-    int ids = page_id(kPagesTC * w + (lane & 3));
-    auto request = [&](int h) {  // the copies of run h, h = w, w + step, ...
-      if (h < n_halves) {
-        const int n = min(kPagesTC, max(0, n_pages - kPagesTC * h));  // its pages
-        mbar_arrive_expect_tx_if(lane == 0, bar, n * Sm::page);
-        const bool there = lane < n;
-        const size_t blk = there ? static_cast<size_t>(ids) * p.Hkv + g : 0;
-        __syncwarp();
-        bulk_g2s_if(there, slot + lane * Sm::page, src + blk * Sm::page, Sm::page, bar, pol);
-        if (isK && lane < kPagesTC) {
-          const uint32_t at = sbase + Sm::sc0 + (h >> 1) % kScaleSlots * Sm::scSlot + ((h & 1) * kPagesTC + lane) * 4;
-          if (there) {
-            fetch4(at, p.ks + blk);
-            fetch4(at + 4 * kPagesB, p.vs + blk);
-          } else {  // no page: zeros (its keys are masked)
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(0) : "memory");
-            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at + 4 * kPagesB), "r"(0) : "memory");
-          }
-        }
-        ids = page_id(kPagesTC * (h + step) + (lane & 3));
-      }
-      fetch_commit();
-    };
-    request(w);
     bool ok = true;
     uint32_t phase = 0;
     int h = w;
@@ -454,33 +479,19 @@ __global__ void __launch_bounds__(BSmem<D, QSPLIT>::threads, 1)
     float* xch = reinterpret_cast<float*>(smem + Sm::xch0);  // [part][row]
     float rs;
     {
-      constexpr int N = D / kParts;
       float x[N];
-      if (valid_row) {
-        const size_t at = (static_cast<size_t>(q0 + rho / p.G) * p.Hq + g * p.G + rho % p.G) * D + N * part;
-        if constexpr (!QSPLIT) {
-          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + at);
 #pragma unroll
-          for (int i = 0; i < N / 8; ++i) {
-            const uint4 v = src[i];
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      for (int i = 0; i < QN; ++i) {
+        const uint32_t w4[4] = {qraw[i].x, qraw[i].y, qraw[i].z, qraw[i].w};
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              x[8 * i + 2 * u] = __uint_as_float(w[u] << 16);
-              x[8 * i + 2 * u + 1] = __uint_as_float(w[u] & 0xffff0000u);
-            }
-          }
-        } else {
-          const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.q) + at);
-#pragma unroll
-          for (int i = 0; i < N / 4; ++i) {
-            const float4 v = src[i];
-            x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+        for (int u = 0; u < 4; ++u) {
+          if constexpr (QSPLIT) {
+            x[4 * i + u] = __uint_as_float(w4[u]);
+          } else {
+            x[8 * i + 2 * u] = __uint_as_float(w4[u] << 16);
+            x[8 * i + 2 * u + 1] = __uint_as_float(w4[u] & 0xffff0000u);
           }
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = 0.f;
       }
       float top = 0.f;
 #pragma unroll
@@ -695,7 +706,7 @@ __global__ void __launch_bounds__(BSmem<D, QSPLIT>::threads, 1)
         float* dst = partial ? p.ws_o + pidx * D
                              : p.out + (static_cast<size_t>(q0 + rho / p.G) * p.Hq + g * p.G + rho % p.G) * D;
         bulk_s2g(dst, orow, D * 4);
-        bulk_store_wait();
+        bulk_store_wait();  // (arrived: a merge reads it, an error found late writes over it)
       }
     }
   }
