@@ -206,6 +206,38 @@ def test_decode_against_the_definition(fp8, Hq, H, D, dtype, window):
 
 
 @pytest.mark.parametrize("fp8", FORMATS, ids=IDS)
+@pytest.mark.parametrize("Hq,H,D", [(8, 4, 64), (6, 2, 128)])
+@pytest.mark.parametrize("window", [0, 21])
+def test_decode_of_more_sequences_than_one_wave_of_wide_blocks(fp8, Hq, H, D, window):
+    """Batches past that take blocks of fewer warps; split or not, rows depend on their own
+    sequence only."""
+    rng = np.random.default_rng(D + window)
+    lens = [int(n) for n in rng.integers(0, 70, 240)]
+    bc, tables = built(rng, lens, H, D, fp8)
+    q = torch.from_numpy(rng.standard_normal((len(lens), Hq, D)).astype(np.float32)).cuda()
+    want, A = R.decode(bc, q.cpu().numpy(), tables, lens, 1 / np.sqrt(D), window)
+    for split in (0, 1, 2):
+        got, status = run_decode(bc, tables, lens, q, window, split)
+        assert status == 0
+        assert np.abs(got - want).max() <= tol(bc, tables, A), split
+
+
+@pytest.mark.parametrize("fp8", FORMATS, ids=IDS)
+@pytest.mark.parametrize("Hq,H,D", [(8, 1, 64), (3, 1, 64), (6, 1, 128)])
+def test_decode_of_many_splits(fp8, Hq, H, D):
+    """Up to 157 partials, joined in batches by all or half of a block's threads."""
+    rng = np.random.default_rng(Hq)
+    lens = [2500, 7, 1290]
+    bc, tables = built(rng, lens, H, D, fp8, spread=0.5)
+    q = torch.from_numpy(rng.standard_normal((len(lens), Hq, D)).astype(np.float32)).to(torch.bfloat16).cuda()
+    want, A = R.decode(bc, q.float().cpu().numpy(), tables, lens, 1 / np.sqrt(D))
+    for split in (0, 1, 2, 5, 9):
+        got, status = run_decode(bc, tables, lens, q, split=split)
+        assert status == 0
+        assert np.abs(got - want).max() <= tol(bc, tables, A), split
+
+
+@pytest.mark.parametrize("fp8", FORMATS, ids=IDS)
 @pytest.mark.parametrize("size", [(1.0, 1e-6), (1.0, 1e6), (1e5, 1.0), (1e-5, 1e-12), (3.0, 1e30)])
 def test_decode_and_prefill_over_the_range_of_values(fp8, size):
     """V (and K) of very small and very large values: nothing leaves FP16's range inside.
