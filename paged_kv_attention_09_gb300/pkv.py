@@ -181,12 +181,18 @@ def _ptr(t: Optional[torch.Tensor]):
 # the current stream's handle without building a Stream object (a microsecond or two per
 # call), where this torch offers it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _current_device() -> int:
+    """torch.cuda.current_device() of a process whose CUDA is initialised."""
+    return torch.cuda.current_device() if _get_device is None else _get_device()
 
 
 def _stream(stream):
     if stream is None:
         if _raw_stream is not None and torch.cuda.is_initialized():
-            return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
+            return ctypes.c_void_p(_raw_stream(_current_device()))
         return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
@@ -544,7 +550,7 @@ def _issue(fn, args, what: str, bound: bool, index: int):
     current device stands: bind and issue it there).  index: the device's number, -1: CPU."""
     if bound:
         return BoundCall(fn, args, what)
-    if index >= 0 and index != torch.cuda.current_device():
+    if index >= 0 and index != _current_device():
         with torch.cuda.device(index):
             code = fn(*args)
     else:
