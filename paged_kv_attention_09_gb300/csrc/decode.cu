@@ -1939,13 +1939,14 @@ bool plan_decode(const CacheView& c, int B, int Hq, int MB, int q_dtype, int dev
   // and wide: 4 ragged contexts of 32k, heads of 128, 18.9 and 16.8; 32 x 2k 13.2 and 12.4;
   // 128 x 1k 16.1 and 13.9; heads of 64: 1 x 32k 19.0 and 14.9, 96 x 1k 17.5 and 13.5, 2 x 1k 8.4
   // and 7.8.  Over one wave: 160 x 1k, heads of 64, 17.6 and 18.9; 200 x 1k, heads of 128, 18.4
-  // and 21.5.)
+  // and 21.5.)  A caller's split fixes the order of the sums on every device, so the choice
+  // then goes by GB300's 152 SMs, not by this device's.
   plan->wide = 0;
   if (block_scaled(c.dtype)) {
     const Variant wv = variant(c.dtype, c.D, step, c.window > 0, true);
     int wocc = 0;
     if (!device_facts(device, wv, &sms, &wocc)) return false;
-    if (units <= static_cast<long long>(sms) * wocc) {
+    if (units <= static_cast<long long>(chunk_override > 0 ? 152 : sms) * wocc) {
       plan->wide = 1;
       v = wv;
       occ = wocc;
